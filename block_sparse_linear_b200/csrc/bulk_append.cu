@@ -142,14 +142,15 @@ bulk_state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     const int b = bh / hkv, h = bh % hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // everything earlier on the stream (the previous call's merge reads this workspace,
+    // its length advance is what the block kernel after this one reads, a block plan
+    // writes the counts) is complete before this kernel reads anything or lets the block
+    // kernel launch
+    pdl_wait();
+    pdl_trigger();
     const int n = bulk_count(n_new, max_new, b);
     const int t0 = split * tsplit;
     const int ntok = max(0, min(n, t0 + tsplit) - t0);
-    // everything earlier on the stream (the previous call's merge reads this workspace,
-    // its length advance is what the block kernel after this one reads) is complete
-    // before this kernel lets the block kernel launch
-    pdl_wait();
-    pdl_trigger();
     if (ntok == 0) return;                          // no partial: the merge skips this split
     const int ntiles = (ntok + kBulkTok - 1) / kBulkTok;
     const int row0 = b * max_new + t0;              // first input row of this split
