@@ -3,8 +3,9 @@
 ``SplaDecodeCache`` holds the device buffers of include/spla.h's ``spla_cache``
 (allocated with PyTorch, which is used for device memory and streams only) and
 forwards ``append`` / ``decode`` to ``spla_append_kv`` (or ``spla_append_kv_bulk``
-for long chunks) / ``spla_decode``. Every
-step of the decode path runs in the library's kernels; there is no fallback.
+for long chunks) / ``spla_decode``. ``paged`` holds the serving calls around it: block
+tables grown on the device, q/k norm with rotation, exact chunk attention. Every
+step runs in the library's kernels; there is no fallback.
 """
 from dataclasses import dataclass
 
@@ -15,8 +16,11 @@ from ._lib import (SPLA_BF16, SPLA_F32, SPLA_FLAG_FIRST_ORDER, SPLA_FLAG_NO_RLA,
                    SPLA_WS_STAMP_BYTES, SplaError, spla_append_bulk_workspace_size, spla_append_kv,
                    spla_append_kv_bulk, spla_cache_init, spla_decode, spla_decode_static_workspace,
                    spla_decode_workspace_size)
+from .paged import BlockPlan, SplaBlockPool, SplaPagedKV, qk_norm_rope
+from .paged import chunk_attention as _chunk_attention
 
-__all__ = ["SplaConfig", "SplaDecodeCache", "SplaError", "spla_append_bulk_workspace_size",
+__all__ = ["BlockPlan", "SplaBlockPool", "SplaConfig", "SplaDecodeCache", "SplaError",
+           "SplaPagedKV", "qk_norm_rope", "spla_append_bulk_workspace_size",
            "spla_append_kv", "spla_append_kv_bulk", "spla_cache_init", "spla_decode",
            "spla_decode_static_workspace", "spla_decode_workspace_size"]
 
@@ -92,6 +96,7 @@ class SplaDecodeCache:
         self._n_new = torch.zeros((batch,), dtype=torch.int32, device=dev)
         self._bulk_ws = None
         self._bc_ws = None
+        self._chunk_ws = None
         spla_cache_init(self.params, self.c, self._stream(stream))
 
     def _stream(self, stream=None) -> int:
@@ -164,6 +169,13 @@ class SplaDecodeCache:
                     ptr(o_sparse), ptr(o_rla), self.workspace.data_ptr(), self.ws_bytes,
                     self.dev_status.data_ptr(), self._stream(stream))
         return out
+
+    def chunk_attention(self, q: torch.Tensor, n_new: torch.Tensor, out: torch.Tensor = None,
+                        lse: torch.Tensor = None, lens: torch.Tensor = None,
+                        stream=None) -> torch.Tensor:
+        """Exact causal attention of each sequence's last n_new appended tokens over all it
+        holds (no selection, no residual): q [batch][max_new][Hq][d]; as SplaPagedKV's."""
+        return _chunk_attention(self, q, n_new, out, lse, lens, stream)
 
     def decode_static_workspace(self, q: torch.Tensor, gamma: torch.Tensor = None,
                                 out: torch.Tensor = None, sel_idx: torch.Tensor = None,

@@ -24,6 +24,7 @@ SPLA_DEV_CAPACITY = 0x2
 SPLA_DEV_TIMEOUT = 0x4
 SPLA_DEV_BAD_COUNT = 0x8
 SPLA_DEV_RLA_UNRESOLVED = 0x10
+SPLA_DEV_NO_BLOCKS = 0x20
 # dtypes and flags
 SPLA_F32 = 0
 SPLA_BF16 = 1
@@ -32,12 +33,15 @@ SPLA_FLAG_FIRST_ORDER = 0x2
 SPLA_MAX_BLOCKS_PER_SEQ = 32768
 SPLA_STATIC_WORKSPACE_BYTES = 16 << 20
 SPLA_WS_STAMP_BYTES = 16384
+SPLA_MAX_PLAN_BATCH = 32768
 
 EXPORTS = ("spla_cache_init", "spla_append_kv", "spla_append_kv_bulk",
            "spla_append_bulk_workspace_size", "spla_decode_workspace_size", "spla_decode",
            "spla_shard_candidates", "spla_shard_partials", "spla_shard_merge",
            "spla_block_causal_workspace_size", "spla_block_causal_forward",
            "spla_decode_static_workspace", "spla_profile_events", "spla_profile_stamps",
+           "spla_block_plan", "spla_block_release", "spla_qk_norm_rope",
+           "spla_chunk_attention_workspace_size", "spla_chunk_attention",
            "spla_status_string", "spla_last_cuda_error", "spla_version")
 
 
@@ -56,6 +60,13 @@ class spla_cache(ctypes.Structure):
                 ("m", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("context_lens", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32), ("num_phys_blocks", ctypes.c_int32)]
+
+
+class spla_block_pool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("free_list", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("num_phys_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32)]
 
 
 class SplaError(RuntimeError):
@@ -94,6 +105,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.spla_block_causal_workspace_size.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
     lib.spla_block_causal_forward.argtypes = [P, C, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp,
                                               vp]
+    BP, i64, f32 = ctypes.POINTER(spla_block_pool), ctypes.c_int64, ctypes.c_float
+    lib.spla_block_plan.argtypes = [BP, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.spla_block_release.argtypes = [BP, vp, vp, vp, vp]
+    lib.spla_qk_norm_rope.argtypes = [P, vp, i64, vp, i64, vp, i64, i64, vp, vp, i32, i32, vp, vp,
+                                      f32, vp, vp, vp, vp, i32, vp, vp]
+    lib.spla_chunk_attention_workspace_size.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
+    lib.spla_chunk_attention.argtypes = [P, C, vp, vp, i32, vp, vp, vp, sz, vp, vp]
     lib.spla_profile_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i32]
     lib.spla_profile_stamps.argtypes = [i32]
     for f in ("spla_cache_init", "spla_append_kv", "spla_append_kv_bulk",
@@ -102,7 +120,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
            "spla_block_causal_workspace_size", "spla_block_causal_forward",
               "spla_decode_static_workspace", "spla_profile_events", "spla_profile_stamps",
               "spla_shard_candidates", "spla_shard_partials", "spla_shard_merge",
-              "spla_block_causal_workspace_size", "spla_block_causal_forward"):
+              "spla_block_causal_workspace_size", "spla_block_causal_forward",
+              "spla_block_plan", "spla_block_release", "spla_qk_norm_rope",
+              "spla_chunk_attention_workspace_size", "spla_chunk_attention"):
         getattr(lib, f).restype = ctypes.c_int
     lib.spla_status_string.argtypes = [ctypes.c_int]
     lib.spla_status_string.restype = ctypes.c_char_p
@@ -217,3 +237,42 @@ def spla_profile_events(events):
     """events: 2 to 8 cudaEvent_t handles (ints), or an empty sequence to stop recording."""
     arr = (ctypes.c_void_p * max(1, len(events)))(*events)
     _check("spla_profile_events", load().spla_profile_events(arr, len(events)))
+
+
+def spla_block_plan(pool, context_lens, n_new, max_new, n_granted, lens_after, positions, slots,
+                    free_out, dev_status, stream=0):
+    _check("spla_block_plan",
+           load().spla_block_plan(ctypes.byref(pool), context_lens, n_new, max_new, n_granted,
+                                  lens_after, positions, slots, free_out, dev_status, stream))
+
+
+def spla_block_release(pool, keep_lens, context_lens, dev_status, stream=0):
+    _check("spla_block_release",
+           load().spla_block_release(ctypes.byref(pool), keep_lens, context_lens, dev_status,
+                                     stream))
+
+
+def spla_qk_norm_rope(params, q, q_stride, k, k_stride, v, v_stride, rows, positions, inv_freq,
+                      rot_dim, interleaved, q_gamma, k_gamma, eps, q_out, k_out, v_out, slots,
+                      num_phys_blocks, dev_status, stream=0):
+    _check("spla_qk_norm_rope",
+           load().spla_qk_norm_rope(ctypes.byref(params), q, q_stride, k, k_stride, v, v_stride,
+                                    rows, positions, inv_freq, rot_dim, interleaved, q_gamma,
+                                    k_gamma, eps, q_out, k_out, v_out, slots, num_phys_blocks,
+                                    dev_status, stream))
+
+
+def spla_chunk_attention_workspace_size(params, batch, max_new) -> int:
+    n = ctypes.c_size_t(0)
+    _check("spla_chunk_attention_workspace_size",
+           load().spla_chunk_attention_workspace_size(ctypes.byref(params), batch, max_new,
+                                                      ctypes.byref(n)))
+    return n.value
+
+
+def spla_chunk_attention(params, cache, q, n_new, max_new, out, lse, workspace, workspace_bytes,
+                         dev_status, stream=0):
+    _check("spla_chunk_attention",
+           load().spla_chunk_attention(ctypes.byref(params), ctypes.byref(cache), q, n_new,
+                                       max_new, out, lse, workspace, workspace_bytes, dev_status,
+                                       stream))

@@ -51,6 +51,15 @@ cudaError_t launch_decode_simt(const CacheView& c, int dtype, const DecodeArgs& 
 cudaError_t launch_combine(const CacheView& c, int dtype, const DecodeArgs& a, cudaStream_t s);
 size_t mma_smem_for(int d, int bs, int max_per);
 size_t simt_smem_for(int d, int bs, int max_per);
+cudaError_t launch_block_plan(const spla_block_pool* pool, const int32_t* lens,
+                              const int32_t* n_new, int32_t max_new, int32_t* n_granted,
+                              int32_t* lens_after, int32_t* positions, int64_t* slots,
+                              int32_t* free_out, int32_t* status, cudaStream_t s);
+cudaError_t launch_block_release(const spla_block_pool* pool, const int32_t* keep_lens,
+                                 int32_t* lens, int32_t* status, cudaStream_t s);
+cudaError_t launch_norm_rope(const RopeArgs& a, int d, int dtype, cudaStream_t s);
+size_t chunk_workspace_bytes(int d, int dtype);
+cudaError_t launch_chunk_simt(const CacheView& c, int dtype, const ChunkArgs& a, cudaStream_t s);
 
 // The split heuristic is tuned for the 148-SM B200 (three decode CTAs per SM);
 // results do not depend on it.
@@ -632,6 +641,176 @@ spla_status spla_block_causal_forward(const spla_params* params, const spla_cach
         params->n_sink, (params->flags & SPLA_FLAG_FIRST_ORDER) ? 1 : 0,
         (params->flags & SPLA_FLAG_NO_RLA) ? 1 : 0, scale, eps, static_cast<char*>(workspace),
         dev_status, (cudaStream_t)stream);
+    return e == cudaSuccess ? SPLA_OK : cuda_fail(e);
+}
+
+// ------------------------------------------------------------------ paged serving
+static bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+static spla_status check_pool(const spla_block_pool* p) {
+    if (!p || !p->block_table || !p->free_list || !p->free_count) return SPLA_ERR_INVALID_ARG;
+    if (p->batch <= 0 || p->max_blocks_per_seq <= 0 || p->num_phys_blocks <= 0)
+        return SPLA_ERR_INVALID_ARG;
+    if (p->block_size != 64 && p->block_size != 128) return SPLA_ERR_UNSUPPORTED;
+    if (p->batch > SPLA_MAX_PLAN_BATCH || p->max_blocks_per_seq > SPLA_MAX_BLOCKS_PER_SEQ)
+        return SPLA_ERR_CAPACITY;
+    return SPLA_OK;
+}
+
+spla_status spla_block_plan(const spla_block_pool* pool, const int32_t* context_lens,
+                            const int32_t* n_new, int32_t max_new, int32_t* n_granted,
+                            int32_t* lens_after, int32_t* positions, int64_t* slots,
+                            int32_t* free_out, int32_t* dev_status, void* stream) {
+    spla_status st = check_pool(pool);
+    if (st != SPLA_OK) return st;
+    if (!context_lens || !n_new || !n_granted || !free_out || max_new < 0 ||
+        lens_after == context_lens || n_granted == context_lens)
+        return SPLA_ERR_INVALID_ARG;
+    if ((int64_t)pool->batch * max_new > INT32_MAX) return SPLA_ERR_CAPACITY;
+    cudaError_t e = launch_block_plan(pool, context_lens, n_new, max_new, n_granted, lens_after,
+                                      positions, slots, free_out, dev_status,
+                                      (cudaStream_t)stream);
+    return e == cudaSuccess ? SPLA_OK : cuda_fail(e);
+}
+
+spla_status spla_block_release(const spla_block_pool* pool, const int32_t* keep_lens,
+                               int32_t* context_lens, int32_t* dev_status, void* stream) {
+    spla_status st = check_pool(pool);
+    if (st != SPLA_OK) return st;
+    if (!keep_lens || !context_lens || keep_lens == context_lens) return SPLA_ERR_INVALID_ARG;
+    cudaError_t e = launch_block_release(pool, keep_lens, context_lens, dev_status,
+                                         (cudaStream_t)stream);
+    return e == cudaSuccess ? SPLA_OK : cuda_fail(e);
+}
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+static bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+spla_status spla_qk_norm_rope(const spla_params* params, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              int64_t rows, const int32_t* positions, const double* inv_freq,
+                              int32_t rot_dim, int32_t interleaved, const float* q_gamma,
+                              const float* k_gamma, float eps, void* q_out, void* k_out,
+                              void* v_out, const int64_t* slots, int32_t num_phys_blocks,
+                              int32_t* dev_status, void* stream) {
+    spla_status st = check_params(params);
+    if (st != SPLA_OK) return st;
+    const int64_t d = params->head_dim, hq = params->num_q_heads, hkv = params->num_kv_heads;
+    const int64_t e = params->dtype == SPLA_BF16 ? 2 : 4;
+    if (rows < 0 || rot_dim < 0) return SPLA_ERR_INVALID_ARG;
+    if (rot_dim > d || rot_dim % 16) return SPLA_ERR_UNSUPPORTED;
+    if (rows == 0) return SPLA_OK;
+    if (!q || !k || !positions || !q_out || !k_out || (rot_dim && !inv_freq) || (v && !v_out))
+        return SPLA_ERR_INVALID_ARG;
+    if (q_stride < hq * d || k_stride < hkv * d || (v && v_stride < hkv * d) ||
+        q_stride * e % 16 || k_stride * e % 16 || (v && v_stride * e % 16))
+        return SPLA_ERR_INVALID_ARG;
+    if (slots && num_phys_blocks <= 0) return SPLA_ERR_INVALID_ARG;
+    if (rows > INT32_MAX || q_stride > INT32_MAX || k_stride > INT32_MAX || v_stride > INT32_MAX)
+        return SPLA_ERR_CAPACITY;
+    if (misaligned16(q) || misaligned16(k) || misaligned16(v) || misaligned16(q_out) ||
+        misaligned16(k_out) || misaligned16(v_out))
+        return SPLA_ERR_INVALID_ARG;
+    // a row's heads are read and written by different threads
+    const void* in[3] = {q, k, v};
+    const uint64_t in_n[3] = {(uint64_t)((rows - 1) * q_stride + hq * d) * e,
+                              (uint64_t)((rows - 1) * k_stride + hkv * d) * e,
+                              (uint64_t)(v ? (rows - 1) * v_stride + hkv * d : 0) * e};
+    const uint64_t kv_n = (uint64_t)(slots ? (int64_t)num_phys_blocks * params->block_size : rows) *
+                          hkv * d * e;
+    const void* out[3] = {q_out, k_out, v ? v_out : nullptr};
+    const uint64_t out_n[3] = {(uint64_t)(rows * hq * d) * e, kv_n, kv_n};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 3; ++j)
+            if (overlap(in[i], in_n[i], out[j], out_n[j])) return SPLA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(out[i], out_n[i], out[j], out_n[j])) return SPLA_ERR_INVALID_ARG;
+    }
+    RopeArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.q_gamma = q_gamma;
+    a.k_gamma = k_gamma;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.slots = slots;
+    a.status = dev_status;
+    a.rows = rows;
+    a.num_slots = (int64_t)num_phys_blocks * params->block_size;
+    a.eps = eps > 0.f ? eps : 1e-6f;
+    a.hq = (int)hq;
+    a.hkv = (int)hkv;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.bs = params->block_size;
+    cudaError_t err = launch_norm_rope(a, params->head_dim, params->dtype, (cudaStream_t)stream);
+    return err == cudaSuccess ? SPLA_OK : cuda_fail(err);
+}
+
+static spla_status check_chunk(const spla_params* params, int32_t batch, int32_t max_new) {
+    spla_status st = check_params(params);
+    if (st != SPLA_OK) return st;
+    if (batch <= 0 || max_new < 0) return SPLA_ERR_INVALID_ARG;
+    if ((int64_t)batch * max_new * params->num_q_heads > INT32_MAX) return SPLA_ERR_CAPACITY;
+    return SPLA_OK;
+}
+
+spla_status spla_chunk_attention_workspace_size(const spla_params* params, int32_t batch,
+                                                int32_t max_new, size_t* bytes) {
+    spla_status st = check_chunk(params, batch, max_new);
+    if (st != SPLA_OK) return st;
+    if (!bytes) return SPLA_ERR_INVALID_ARG;
+    *bytes = chunk_workspace_bytes(params->head_dim, params->dtype);
+    return SPLA_OK;
+}
+
+spla_status spla_chunk_attention(const spla_params* params, const spla_cache* cache,
+                                 const void* q, const int32_t* n_new, int32_t max_new, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes,
+                                 int32_t* dev_status, void* stream) {
+    spla_status st = check_params(params);
+    if (st != SPLA_OK) return st;
+    if (!cache || !cache->k_pool || !cache->v_pool || !cache->block_table ||
+        !cache->context_lens || cache->max_blocks_per_seq <= 0 || cache->num_phys_blocks <= 0)
+        return SPLA_ERR_INVALID_ARG;
+    if (cache->max_blocks_per_seq > SPLA_MAX_BLOCKS_PER_SEQ) return SPLA_ERR_CAPACITY;
+    if ((st = check_chunk(params, cache->batch, max_new)) != SPLA_OK) return st;
+    if (!n_new) return SPLA_ERR_INVALID_ARG;
+    if (max_new == 0) return SPLA_OK;
+    if (!q || !out || misaligned16(q) || misaligned16(out) || misaligned16(cache->k_pool) ||
+        misaligned16(cache->v_pool))
+        return SPLA_ERR_INVALID_ARG;
+    const CacheView v = view_of(params, cache);
+    if ((int64_t)v.num_phys * v.hkv * v.bs > INT32_MAX) return SPLA_ERR_CAPACITY;
+    // q and out are read and written by different thread blocks
+    const uint64_t qn = (uint64_t)v.batch * max_new * v.hq * v.d *
+                        (params->dtype == SPLA_BF16 ? 2 : 4);
+    if (overlap(q, qn, out, qn)) return SPLA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < chunk_workspace_bytes(v.d, params->dtype) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return SPLA_ERR_WORKSPACE;
+    const double scale = params->softmax_scale > 0.f ? (double)params->softmax_scale
+                                                     : 1.0 / sqrt((double)params->head_dim);
+    ChunkArgs a;
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.n_new = n_new;
+    a.status = dev_status;
+    a.ws = static_cast<char*>(workspace);
+    a.max_new = max_new;
+    a.sl2 = (float)(scale * 1.4426950408889634);
+    cudaError_t e = launch_chunk_simt(v, params->dtype, a, (cudaStream_t)stream);
     return e == cudaSuccess ? SPLA_OK : cuda_fail(e);
 }
 

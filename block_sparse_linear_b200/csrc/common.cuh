@@ -88,6 +88,38 @@ struct DecodeArgs {
     float sl2, eps;
 };
 
+// Arguments of the chunk-attention kernels beyond the cache.
+struct ChunkArgs {
+    const void* q;              // [batch][max_new][Hq][d]
+    void* out;                  // same layout
+    float* lse;                 // [batch][max_new][Hq] or null
+    const int32_t* n_new;       // [batch]
+    int32_t* status;
+    char* ws;
+    int32_t max_new;
+    float sl2;                  // softmax scale * log2(e)
+};
+
+// Arguments of the norm + rotation kernel.
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* v;                 // or null
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* positions;      // [rows]
+    const double* inv_freq;        // [rot/2]
+    const float* q_gamma;          // [d] or null (no norm)
+    const float* k_gamma;
+    void* q_out;
+    void* k_out;                   // [rows][hkv][d], or the pools when slots is set
+    void* v_out;
+    const int64_t* slots;          // or null
+    int32_t* status;
+    int64_t rows, num_slots;
+    float eps;
+    int hq, hkv, rot, interleaved, bs;
+};
+
 // Partial record of one decode CTA for one query head:
 //   [0] m (running max, log2 units), [1] l (softmax denominator),
 //   [2] D~_part, [3] unused, [4..4+d) acc, [4+d..4+2d) N~_part

@@ -67,6 +67,8 @@ typedef enum {
 #define SPLA_DEV_BAD_COUNT       0x8   /* n_new[b] outside [0, max_new] */
 #define SPLA_DEV_RLA_UNRESOLVED  0x10  /* a head's residual denominator D - D~ was not positive:
                                           its o_rla was set to 0 (see spla_decode) */
+#define SPLA_DEV_NO_BLOCKS       0x20  /* spla_block_plan: the free blocks ran out; the requests
+                                          they did not reach were granted nothing */
 
 typedef enum { SPLA_F32 = 0, SPLA_BF16 = 1 } spla_dtype;
 
@@ -311,6 +313,143 @@ SPLA_API spla_status spla_block_causal_forward(const spla_params* params, const 
                                       int32_t max_len, const float* rms_gamma, void* out,
                                       float* o_sparse_dbg, float* o_rla_dbg, void* workspace,
                                       size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * ---- Paged serving: block tables, q/k norm with rotation, chunk attention ----
+ * What a serving step does around the appends and the sparse decode: grow the block
+ * tables on the device, bring the projection's q and k into the form that the cache
+ * holds, and attend exactly (every token, no selection) where a layer or a chunk asks
+ * for it. The pages speak of a paged cache (mlsanity, on PagedAttention) and of exact
+ * softmax attention (Baidu, section 1); the calls are the library's own.
+ *
+ * The pool of KV blocks. One block table and one pool may serve the caches of many
+ * layers: every layer's k_pool and v_pool are indexed by the same physical blocks.
+ *   block_table : [batch][max_blocks_per_seq] int32, logical -> physical.
+ *   free_list   : [num_phys_blocks] int32, a stack: entries 0 .. *free_count - 1 are the
+ *                 blocks no sequence holds.
+ *   free_count  : [1] int32.
+ */
+typedef struct {
+    int32_t* block_table;
+    int32_t* free_list;
+    int32_t* free_count;
+    int32_t batch;
+    int32_t max_blocks_per_seq;
+    int32_t num_phys_blocks;
+    int32_t block_size;          /* 64 or 128 */
+} spla_block_pool;
+
+/* Largest batch spla_block_plan and spla_block_release take. */
+#define SPLA_MAX_PLAN_BATCH 32768
+
+/*
+ * Give every sequence the blocks its new tokens need, and say where they go.
+ *   context_lens : [batch] tokens held (not changed: the append advances them).
+ *   n_new        : [batch] new tokens asked for, each in [0, max_new].
+ *   n_granted    : [batch] out: n_new[b], or 0 where the request is refused. It is the
+ *                  n_new of the append or attention that follows; it may be the n_new
+ *                  buffer itself.
+ *   lens_after   : [batch] out or NULL: context_lens[b] + n_granted[b]; not the
+ *                  context_lens buffer.
+ *   positions    : [batch][max_new] out or NULL: the new tokens' positions, -1 past
+ *                  n_granted[b].
+ *   slots        : [batch][max_new] int64 out or NULL: physical block * block_size +
+ *                  offset, -1 past n_granted[b].
+ *   free_out     : [1] out: the blocks left. The pool's free_count itself to take the
+ *                  blocks; another word to look ahead: the table rows and outputs are
+ *                  written, but the blocks stay on the stack and a later plan hands out
+ *                  the same ones again.
+ * Sequences are served in index order, blocks from the top of the stack. A sequence that
+ * needs no new block is always granted. Once a request does not fit, it and every later
+ * one that needs a block are refused whole and SPLA_DEV_NO_BLOCKS is set (none is
+ * overtaken). A count outside [0, max_new] sets SPLA_DEV_BAD_COUNT, a length outside the
+ * table or an append past it SPLA_DEV_CAPACITY; that sequence is granted 0. A slot whose
+ * table entry is not a physical block is -1 and sets SPLA_DEV_BAD_BLOCK_TABLE. A
+ * free_count outside [0, num_phys_blocks] sets SPLA_DEV_CAPACITY and counts as 0.
+ */
+SPLA_API spla_status spla_block_plan(const spla_block_pool* pool, const int32_t* context_lens,
+                                     const int32_t* n_new, int32_t max_new, int32_t* n_granted,
+                                     int32_t* lens_after, int32_t* positions, int64_t* slots,
+                                     int32_t* free_out, int32_t* dev_status, void* stream);
+
+/*
+ * Shorten sequences to keep_lens[b] tokens (0 ends a request; a shorter draft gives back
+ * what verification rejected) and push the blocks past them on the stack, in index and
+ * table order; their table entries become -1 and context_lens[b] = keep_lens[b].
+ * keep_lens[b] >= context_lens[b] leaves the sequence as it is. A negative keep_lens[b]
+ * sets SPLA_DEV_BAD_COUNT, a length outside the table SPLA_DEV_CAPACITY, an entry that is
+ * not a physical block SPLA_DEV_BAD_BLOCK_TABLE, more blocks than the pool has
+ * SPLA_DEV_CAPACITY; each leaves that sequence (the last also the later ones that give
+ * blocks back) unchanged. Only lengths and blocks change: statistics and the
+ * linear-attention state of a spla_cache still hold what was appended, so a cache whose
+ * layers decode sparsely releases whole sequences only.
+ */
+SPLA_API spla_status spla_block_release(const spla_block_pool* pool, const int32_t* keep_lens,
+                                        int32_t* context_lens, int32_t* dev_status, void* stream);
+
+/*
+ * RMSNorm of each query and key head and the rotary position, one pass.
+ *   q, k, v     : row r of the projection's output: Hq (Hkv, Hkv) heads of d elements side
+ *                 by side from q + r * q_stride (strides in elements; rows of one fused
+ *                 tensor or of three), params->dtype. v may be NULL.
+ *   rows        : host, >= 0.
+ *   positions   : [rows] int32; a row with a negative one is skipped, its outputs left.
+ *   inv_freq    : [rot_dim / 2] double: radians per position of each pair.
+ *   rot_dim     : 0 .. d, a multiple of 16: the first rot_dim elements of a head are
+ *                 rotated, pair i being (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ *                 interleaved != 0. 0: no rotation (inv_freq may be NULL).
+ *   q_gamma, k_gamma : [d] fp32 norm scales; NULL: that side is not normed.
+ *   eps         : added to the mean square; <= 0: 1e-6.
+ *   q_out       : [rows][Hq][d].
+ *   k_out, v_out: [rows][Hkv][d] (what spla_append_kv reads) when slots is NULL;
+ *                 otherwise the pools [num_phys_blocks][Hkv][block_size][d], written at
+ *                 slots[r] (spla_block_plan). A negative slot writes no key or value; one
+ *                 past the pool sets SPLA_DEV_BAD_BLOCK_TABLE and writes none. Slots are
+ *                 distinct. v_out may be NULL when v is.
+ * Angles are taken in 64 bits, norms and rotations in 32, each output rounded once.
+ * q, k, v, the outputs and gammas (read element by element) may not overlap the outputs;
+ * q, k, v, q_out, k_out, v_out 16-byte aligned and strides a multiple of 16 bytes
+ * (SPLA_ERR_INVALID_ARG otherwise). num_phys_blocks is read only with slots.
+ */
+SPLA_API spla_status spla_qk_norm_rope(const spla_params* params, const void* q, int64_t q_stride,
+                                       const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, int64_t rows, const int32_t* positions,
+                                       const double* inv_freq, int32_t rot_dim,
+                                       int32_t interleaved, const float* q_gamma,
+                                       const float* k_gamma, float eps, void* q_out, void* k_out,
+                                       void* v_out, const int64_t* slots, int32_t num_phys_blocks,
+                                       int32_t* dev_status, void* stream);
+
+/*
+ * Exact causal attention of each sequence's last n_new[b] tokens over all it holds: a
+ * chunk of a prompt, the drafts a verification step scores, or (n_new = 1) one decoded
+ * token; the layers that keep full attention, beside the sparse ones.
+ *   cache  : its pools, block_table and context_lens (the chunk's own tokens included)
+ *            are read; blk_stats, S, z and m may be NULL. top_k, n_sink, n_local and
+ *            flags of params are not used.
+ *   q      : [batch][max_new][Hq][d]; query t of sequence b stands at position
+ *            context_lens[b] - n_new[b] + t and sees the tokens up to its own.
+ *   n_new  : [batch] int32 (device), each in [0, min(max_new, context_lens[b])].
+ *   out    : [batch][max_new][Hq][d]; rows t >= n_new[b] are not written.
+ *   lse    : [batch][max_new][Hq] fp32 or NULL: the natural log of each row's sum of
+ *            exponentials (to merge with attention over other tokens).
+ *   workspace : device scratch of at least spla_chunk_attention_workspace_size bytes,
+ *            256-byte aligned, no initialisation; calls that share it are ordered on the
+ *            GPU (one stream, or events), captured ones too.
+ * Tokens past a sequence's length, and tokens after a query's own, have no part in its
+ * result, whatever their slots hold. A count or length out of range sets
+ * SPLA_DEV_BAD_COUNT or SPLA_DEV_CAPACITY and that sequence's rows are not written; a
+ * table entry that is not a physical block sets SPLA_DEV_BAD_BLOCK_TABLE and its tokens
+ * count as zero keys and values.
+ */
+SPLA_API spla_status spla_chunk_attention_workspace_size(const spla_params* params, int32_t batch,
+                                                         int32_t max_new, size_t* bytes);
+
+SPLA_API spla_status spla_chunk_attention(const spla_params* params, const spla_cache* cache,
+                                          const void* q, const int32_t* n_new, int32_t max_new,
+                                          void* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, int32_t* dev_status,
+                                          void* stream);
 
 /*
  * Bytes of the library-owned scratch that spla_decode_static_workspace uses
