@@ -60,6 +60,8 @@ cudaError_t launch_block_release(const spla_block_pool* pool, const int32_t* kee
 cudaError_t launch_norm_rope(const RopeArgs& a, int d, int dtype, cudaStream_t s);
 size_t chunk_workspace_bytes(int d, int dtype);
 cudaError_t launch_chunk_simt(const CacheView& c, int dtype, const ChunkArgs& a, cudaStream_t s);
+cudaError_t launch_chunk_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
+                            const CUtensorMap& tv, const ChunkArgs& a, cudaStream_t s);
 
 // The split heuristic is tuned for the 148-SM B200 (three decode CTAs per SM);
 // results do not depend on it.
@@ -238,6 +240,22 @@ static bool make_input_map(CUtensorMap* m, const void* x, const CacheView& c, in
     cuuint32_t box[3] = {64u, 1u, 64u};
     cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// 3-D view of chunk queries [batch*max_new rows][Hq][d] bf16; box = 64 dims x the G heads of a
+// KV head x 128 / G tokens (16 KiB, the 128 rows of an MMA tile), 128B swizzle; rows past
+// the end read as zero.
+static bool make_query_map(CUtensorMap* m, const void* q, const CacheView& c, int32_t max_new) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)c.hq, (cuuint64_t)c.batch * max_new};
+    cuuint64_t strides[2] = {(cuuint64_t)c.d * 2, (cuuint64_t)c.hq * c.d * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)c.group, 128u / (cuuint32_t)c.group};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
@@ -810,7 +828,16 @@ spla_status spla_chunk_attention(const spla_params* params, const spla_cache* ca
     a.ws = static_cast<char*>(workspace);
     a.max_new = max_new;
     a.sl2 = (float)(scale * 1.4426950408889634);
-    cudaError_t e = launch_chunk_simt(v, params->dtype, a, (cudaStream_t)stream);
+    cudaError_t e;
+    if (params->dtype == SPLA_BF16) {
+        CUtensorMap tq, tk, tv;
+        if (!make_query_map(&tq, q, v, max_new) || !make_pool_map(&tk, v.k_pool, v) ||
+            !make_pool_map(&tv, v.v_pool, v))
+            return cuda_fail(cudaErrorInvalidValue);
+        e = launch_chunk_tc(v, tq, tk, tv, a, (cudaStream_t)stream);
+    } else {
+        e = launch_chunk_simt(v, params->dtype, a, (cudaStream_t)stream);
+    }
     return e == cudaSuccess ? SPLA_OK : cuda_fail(e);
 }
 

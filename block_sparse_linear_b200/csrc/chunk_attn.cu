@@ -86,7 +86,11 @@ chunk_simt_kernel(CacheView c, ChunkArgs a) {
     if (a.lse && lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
-size_t chunk_workspace_bytes(int, int) { return 256; }
+size_t chunk_tc_workspace_bytes(int d);
+
+size_t chunk_workspace_bytes(int d, int dtype) {
+    return dtype == SPLA_BF16 ? chunk_tc_workspace_bytes(d) : 256;
+}
 
 cudaError_t launch_chunk_simt(const CacheView& c, int dtype, const ChunkArgs& a, cudaStream_t s) {
     const int64_t rows = (int64_t)c.batch * a.max_new * c.hq;

@@ -1,0 +1,896 @@
+// Chunk attention, bf16: the products on tcgen05 with logits, probabilities and outputs
+// in tensor memory. chunk_attn.cu states the mathematics.
+//
+// Rows. The G query heads that share a KV head and consecutive new tokens make the 128
+// rows of an MMA tile (row = token * G + head), so a tile of K and V is read once for
+// all of them. A unit is one (sequence, KV head, block of queries): two such tiles
+// (kTwo), or one where the whole chunk fits into it (n_new * G <= 128, decode included).
+//
+// Split. Every unit takes T = ceil(visible tokens / 128) steps over 128-token tiles of K
+// and V. All units' steps in a row, sum T = W of them, are cut into equal runs of
+// C = ceil(W / gridDim) steps, one per CTA (one CTA per SM), whatever the lengths: a
+// single long sequence, a ragged batch and many short prompts all fill the GPU evenly.
+// A unit that lies within one run is finished there; one that is cut leaves unnormalised
+// partial sums (O, l, and the maximum m they are scaled by), which
+// chunk_combine_kernel joins.
+//
+// Warps. 0-3 and 4-7: softmax of query tile 0 and 1 (one row per thread); 8: TMA (K and V
+// tiles page by page into a ring, query tiles; no multicast); 9: issues the MMAs;
+// 10-11: look over the V tiles that some row does not see whole.
+//   S = Q K^T       M128 N128 Kd, both operands in shared memory as TMA wrote them
+//   P = exp2(sl2 S - m), rounded to bf16 over S's columns in tensor memory
+//   O += P V        M128 Nd K128, P from tensor memory, V as TMA wrote it (N-major)
+// The two query tiles alternate on the tensor pipe: one's products run while the other's
+// softmax does. With a single tile S is double-buffered instead.
+// The maximum a row's sums are scaled by follows the running maximum only when that has
+// grown by more than 2^8: until then the sums are merely larger, not less exact, and
+// the rescale of O (a pass over tensor memory) is skipped. l sums the probabilities
+// before they are rounded; the products see them rounded to bf16 (half a step, 2^-8
+// relative, averaged over the tokens), which is what the MMA's operand type allows
+// without a second product.
+//
+// Tokens past the sequence's end may be anything, NaN included, and so may tokens that
+// come after a row's own: logits there are replaced by -inf. Their V rows meet a
+// probability of zero, but 0 * inf is NaN: rows past the end are zeroed in the tile, and
+// in tiles on the diagonal infinities and NaN are taken out of V and noted per dimension
+// (the first token that holds one, by kind), and the epilogue adds them to the rows that
+// see that token.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace spla {
+
+constexpr int kTcThreads = 384;
+constexpr int kTcTile = 128;                 // KV tokens of a step
+constexpr int kTcSmem = 227 * 1024;
+constexpr float kTcLazy = 8.f;               // log2 growth of a maximum that is let stand
+
+template <int D, bool kTwo>
+struct TcShape {
+    static constexpr int kQTiles = kTwo ? 2 : 1;
+    static constexpr int kHalves = D / 64;                   // 64-dimension boxes across a row
+    static constexpr int kTileBytes = kTcTile * D * 2;       // a K, V or Q tile
+    static constexpr int kBox = 8192;                        // 64 tokens x 64 dims
+    static constexpr int kCtl = 2048;                        // barriers and notes
+    static constexpr int kFit = (kTcSmem - 1024 - kCtl - kQTiles * kTileBytes) / kTileBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr int kRows = 128 * kQTiles;
+    static constexpr size_t kSmem = 1024 + kCtl + (size_t)(kQTiles + kStages) * kTileBytes;
+    static_assert(kStages >= 4, "the ring holds two steps");
+    static_assert(kSmem <= kTcSmem, "shared memory");
+};
+
+// What the split's run c left for the join, at its place in the workspace.
+struct ChunkCut {
+    int32_t parts;            // runs the unit that starts in run c and leaves it spans; 0: none
+    int32_t rows;             // its rows that hold queries
+    int32_t b, h, t0;         // sequence, KV head, first query token
+    int32_t pad[3];
+};
+
+constexpr int kMaxRuns = kNumSms;
+constexpr size_t kCutBytes = (sizeof(ChunkCut) * kMaxRuns + 255) / 256 * 256;
+// One partial: O [rows][d], then m [rows], l [rows]; run c has two (0: of the unit it
+// begins inside of, 1: of the unit it leaves unfinished).
+__host__ __device__ constexpr int64_t part_floats(int d) { return 256 * (int64_t)(d + 2); }
+
+size_t chunk_tc_workspace_bytes(int d) {
+    return kCutBytes + (size_t)kMaxRuns * 2 * part_floats(d) * sizeof(float);
+}
+
+// ------------------------------------------------------------------ tcgen05 plumbing
+__device__ __forceinline__ void tcf_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tcf_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle, 1024-byte aligned 8-row atoms
+// (version 1). K-major: rows of 64 elements, 8-row groups 1024 bytes apart. MN-major:
+// 64-element atoms `lbo` bytes apart, 8-row groups of K 1024 bytes apart.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// kind::f16, fp32 accumulator, bf16 operands, A K-major, M = 128.
+constexpr uint32_t tc_idesc(int n, bool b_mn_major) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(smem_u32(bar)) : "memory");
+}
+
+// 32 consecutive columns of this thread's TMEM lane; the caller waits.
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+           "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+           "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+           "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+           "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr) : "memory");
+}
+// Waits for the loads of this thread; the values pass through, so that no use of them
+// can move above the wait.
+__device__ __forceinline__ void tm_tie(float* v) {
+    asm volatile(""
+        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+          "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+          "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+          "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+          "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
+          "+f"(v[31]) :: "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_wait_ld(float* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tm_tie(v + i);
+}
+__device__ __forceinline__ void tm_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* bar, int32_t x,
+                                       int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        :: "r"(smem_u32(dst)), "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ the split
+// The chunk of sequence b; n = 0 where there is none or it is out of range.
+__device__ __forceinline__ void tc_chunk_of(const CacheView& c, const ChunkArgs& a, int b,
+                                            int32_t* L, int32_t* n, bool flag) {
+    *L = c.lens[b];
+    *n = a.n_new[b];
+    int32_t bad = 0;
+    if (*n < 0 || *n > a.max_new) bad = SPLA_DEV_BAD_COUNT;
+    else if (*L < 0 || *L > (int64_t)c.mbp * c.bs) bad = SPLA_DEV_CAPACITY;
+    else if (*n > *L) bad = SPLA_DEV_BAD_COUNT;
+    if (bad) {
+        if (flag) set_status(a.status, bad);
+        *n = 0;
+        *L = 0;
+    }
+}
+
+// Steps of the units before query block qb of a sequence whose chunk starts at position
+// base: sum over i < qb of ceil((base + (i+1) U) / 128), U = 64, 128 or 256.
+__device__ __forceinline__ int64_t steps_before(int64_t base, int64_t qb, int U) {
+    if (U >= 128) {
+        const int64_t k = U / 128;
+        return qb * ((base + 127) / 128) + k * (qb * (qb + 1) / 2);
+    }
+    const int64_t ne = (qb + 1) / 2, no = qb / 2;
+    return ne * ((base + 64 + 127) / 128) + ne * (ne - 1) / 2 +
+           no * ((base + 128 + 127) / 128) + no * (no - 1) / 2;
+}
+
+// A place in the row of all units' steps, and the walk over it that every role makes.
+struct Walk {
+    int b, h, qb;             // unit
+    int32_t L, n;             // its sequence's length and chunk
+    int j;                    // next step of the unit
+    int64_t left;             // steps left in this run
+    int j0, j1, T;            // the current segment [j0, j1) of the unit's T steps
+
+    __device__ __forceinline__ int units(int U) const { return (n + U - 1) / U; }
+    // Next segment of this run; false at its end.
+    __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int U) {
+        if (left <= 0) return false;
+        if (j < 0) {                                  // the last unit is done: go to the next
+            j = 0;
+            if (++qb >= units(U)) {
+                qb = 0;
+                if (++h >= c.hkv) {
+                    h = 0;
+                    n = 0;
+                    while (n == 0) {
+                        if (++b >= c.batch) return false;
+                        tc_chunk_of(c, a, b, &L, &n, false);
+                    }
+                }
+            }
+        }
+        T = (L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + kTcTile - 1) / kTcTile;
+        j0 = j;
+        j1 = (int)min((int64_t)T, j0 + left);
+        left -= j1 - j0;
+        j = j1 < T ? j1 : -1;
+        return true;
+    }
+    // Position of the first query of tile w, and the steps that tile takes part in.
+    __device__ __forceinline__ int tile_end(int w, int per_tile, int U) const {
+        const int64_t t0 = (int64_t)qb * U + (int64_t)w * per_tile;
+        if (t0 >= n) return 0;
+        const int64_t last = L - n + min(t0 + per_tile, (int64_t)n);
+        return min(j1, (int)((last + kTcTile - 1) / kTcTile));
+    }
+};
+
+struct TcNotes {                              // control block in shared memory
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], care_ask, care_done, fin;
+    int64_t scan[kTcThreads / 32];
+    Walk start;
+    int64_t run;                              // C
+    uint32_t tmem;
+    int32_t nf_seg;                           // segment whose infinities and NaN are noted
+    int32_t epi;                              // warps past an epilogue, over all segments
+    int32_t first[3][128];                    // first token with +inf, -inf, NaN, per dimension
+};
+static_assert(sizeof(TcNotes) <= 2048, "control block");
+
+// Bounded waits. A role may sit out another's whole run (thousands of steps), so the
+// bound is a time, looked at every 1024 polls, with a count over it.
+constexpr uint32_t kTcPolls = 1u << 28;
+constexpr unsigned long long kTcWaitNs = 5000000000ull;
+__device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, int32_t* status) {
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 1; i < kTcPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 1023u) == 0 && global_ns() - t0 > kTcWaitNs) break;
+    }
+    set_status(status, SPLA_DEV_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return tc_wait_long(bar, parity, status);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+template <int D, bool kTwo>
+__global__ void __launch_bounds__(kTcThreads, 1)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const CacheView c, const ChunkArgs a) {
+    using S = TcShape<D, kTwo>;
+    extern __shared__ unsigned char tc_smem_raw[];
+    unsigned char* smem = tc_smem_raw + ((1024u - (smem_u32(tc_smem_raw) & 1023u)) & 1023u);
+    unsigned char* qtile = smem;
+    unsigned char* ring = smem + S::kQTiles * S::kTileBytes;
+    TcNotes* nt = reinterpret_cast<TcNotes*>(ring + S::kStages * S::kTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = c.group;
+    const int per_tile = 128 / G;                      // query tokens of a tile
+    const int U = per_tile * S::kQTiles;
+
+    if (tid == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&nt->kv_full[s], 1);
+            mbar_init(&nt->kv_empty[s], 1);
+        }
+        mbar_init(&nt->q_full, 1);
+        mbar_init(&nt->q_empty, 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&nt->s_full[w], 1);
+            mbar_init(&nt->p_full[w], 4);
+            mbar_init(&nt->o_done[w], 1);
+        }
+        mbar_init(&nt->care_ask, 1);
+        mbar_init(&nt->care_done, 2);
+        mbar_init(&nt->fin, 1);
+        fence_barrier_init();
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+        nt->nf_seg = -1;
+        nt->epi = 0;
+        nt->start.left = 0;
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_u32(&nt->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this run's place: contiguous sequences per thread, a scan over the CTA
+    const int per = (c.batch + kTcThreads - 1) / kTcThreads;
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= c.batch) break;
+        int32_t L, n;
+        tc_chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
+        if (n) {
+            const int64_t q = (n + U - 1) / U;
+            mine += c.hkv * (steps_before(L - n, q - 1, U) + (L + kTcTile - 1) / kTcTile);
+        }
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) nt->scan[warp] = upto;
+    tcf_before();
+    __syncthreads();
+    tcf_after();
+    int64_t W = 0;
+    for (int w = 0; w < kTcThreads / 32; ++w) {
+        if (w < warp) upto += nt->scan[w];
+        W += nt->scan[w];
+    }
+    const int64_t C = (W + gridDim.x - 1) / gridDim.x;
+    const int64_t f0 = (int64_t)blockIdx.x * C;
+    if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
+        int64_t at = f0 - (upto - mine);
+        Walk w;
+        for (int i = 0; i < per; ++i) {
+            w.b = tid * per + i;
+            tc_chunk_of(c, a, w.b, &w.L, &w.n, false);
+            if (!w.n) continue;
+            const int64_t q = w.units(U), base = w.L - w.n;
+            const int64_t one = steps_before(base, q - 1, U) + (w.L + kTcTile - 1) / kTcTile;
+            if (at >= one * c.hkv) {
+                at -= one * c.hkv;
+                continue;
+            }
+            w.h = (int)(at / one);
+            at -= w.h * one;
+            int64_t lo = 0, hi = q - 1;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) / 2;
+                if (steps_before(base, mid, U) <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            w.qb = (int)lo;
+            w.j = (int)(at - steps_before(base, lo, U));
+            break;
+        }
+        w.left = min(C, W - f0);
+        nt->start = w;
+        nt->run = C;
+    }
+    __syncthreads();
+    const uint32_t tmem = nt->tmem;
+    Walk wk = nt->start;
+
+    if (warp == 8) {
+        // ---------------------------------------------------------- TMA producer
+        int it = 0, seg = 0;                            // ring slots filled, segments
+        bool ok = true;
+        const int32_t none = (int32_t)((int64_t)c.num_phys * c.hkv * c.bs);   // reads as zeros
+        const int upb = c.bs / 64;                      // 64-token rows of a page
+        while (ok && wk.next(c, a, U)) {
+            if (seg > 0) ok = tc_wait(&nt->q_empty, (seg - 1) & 1, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&nt->q_full, S::kQTiles * S::kTileBytes);
+                for (int w = 0; w < S::kQTiles; ++w)
+                    for (int x = 0; x < S::kHalves; ++x)
+                        tma_q3(qtile + w * S::kTileBytes + x * 16384, &tq, &nt->q_full, 64 * x,
+                               wk.h * G, wk.b * a.max_new + wk.qb * U + w * per_tile);
+            }
+            const int32_t* row = c.table + (int64_t)wk.b * c.mbp;
+            const int nu = (wk.L + 63) / 64;            // 64-token rows the sequence holds
+            int32_t ys = none;
+            for (int j = wk.j0; j < wk.j1; ++j) {
+                const int k = (j - wk.j0) & 15;
+                if (k == 0) {                           // 16 steps' page rows at a time
+                    const int u = 2 * j + lane;
+                    ys = none;
+                    if (u < nu) {
+                        const int32_t phys = row[u / upb];
+                        if (phys >= 0 && phys < c.num_phys)
+                            ys = (phys * c.hkv + wk.h) * c.bs + (u % upb) * 64;
+                        else
+                            set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
+                    }
+                }
+                const int32_t y0 = __shfl_sync(0xffffffffu, ys, 2 * k);
+                const int32_t y1 = __shfl_sync(0xffffffffu, ys, 2 * k + 1);
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const int s = it % S::kStages;
+                    if (it >= S::kStages)
+                        ok = tc_wait(&nt->kv_empty[s], (it / S::kStages - 1) & 1, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        unsigned char* st = ring + s * S::kTileBytes;
+                        mbar_arrive_expect_tx(&nt->kv_full[s], S::kTileBytes);
+                        for (int x = 0; x < S::kHalves; ++x) {
+                            tma_load_2d(st + x * 16384, kv ? &tv : &tk, &nt->kv_full[s], 64 * x, y0);
+                            tma_load_2d(st + x * 16384 + 8192, kv ? &tv : &tk, &nt->kv_full[s],
+                                        64 * x, y1);
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+            ++seg;
+        }
+        // the copies in flight have landed before the CTA may leave
+        for (int i = max(0, it - S::kStages); i < it; ++i)
+            mbar_wait_bounded(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1);
+        if (seg > 0) mbar_wait_bounded(&nt->q_full, (seg - 1) & 1);
+    } else if (warp == 9) {
+        // ---------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t kIdS = tc_idesc(128, false), kIdO = tc_idesc(D, true);
+            const uint32_t q0 = smem_u32(qtile), r0 = smem_u32(ring);
+            int it = 0, seg = 0, cares = 0;
+            int ps[2] = {0, 0};                         // probabilities taken, per buffer
+            bool ok = true;
+            auto full = [&](int i) {
+                const bool r = tc_wait(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1, a.status);
+                tcf_after();
+                return r;
+            };
+            auto do_s = [&](int w, int buf, int i) {    // S of query tile w by ring slot i
+                const uint32_t kt = r0 + (i % S::kStages) * S::kTileBytes;
+                const uint32_t qt = q0 + w * S::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
+                    mma_ss(tmem + 128 * buf, tc_desc(qt + off, 16), tc_desc(kt + off, 16), kIdS,
+                           kk != 0);
+                }
+                tc_commit(&nt->s_full[buf]);
+            };
+            auto do_o = [&](int w, int buf, int i, bool first) {
+                const uint32_t vt = r0 + (i % S::kStages) * S::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kTcTile / 16; ++kk)
+                    mma_ts(tmem + 256 + 128 * w, tmem + 128 * buf + 8 * kk,
+                           tc_desc(vt + kk * 2048, 16384), kIdO, !first || kk != 0);
+            };
+            auto p_wait = [&](int buf) {
+                const bool r = tc_wait(&nt->p_full[buf], ps[buf] & 1, a.status);
+                ++ps[buf];
+                tcf_after();
+                return r;
+            };
+            auto v_wait = [&](int j, int i) {           // V of step j is in and looked over
+                if (!full(i)) return false;
+                if ((int64_t)(j + 1) * kTcTile > wk.L - wk.n + (int64_t)wk.qb * U + 1) {
+                    mbar_arrive(&nt->care_ask);
+                    const bool r = tc_wait(&nt->care_done, cares & 1, a.status);
+                    ++cares;
+                    tcf_after();
+                    return r;
+                }
+                return true;
+            };
+            int buf = 0;                                // S buffer of the next step (one tile)
+            while (ok && wk.next(c, a, U)) {
+                ok = tc_wait(&nt->q_full, seg & 1, a.status);
+                if (!ok) break;
+                ++seg;
+                tcf_after();
+                const int nj = wk.j1 - wk.j0;
+                if constexpr (kTwo) {
+                    const int e[2] = {wk.tile_end(0, per_tile, U), wk.tile_end(1, per_tile, U)};
+                    // slot it + 2 i is K of step i, it + 2 i + 1 its V
+                    if (!(ok = full(it))) break;
+                    for (int w = 0; w < 2; ++w)
+                        if (wk.j0 < e[w]) do_s(w, w, it);
+                    tc_commit(&nt->kv_empty[it % S::kStages]);
+                    if (nj == 1) tc_commit(&nt->q_empty);
+                    for (int i = 0; i < nj && ok; ++i) {
+                        const int j = wk.j0 + i, iv = it + 2 * i + 1, ik = iv + 1;
+                        if (!(ok = v_wait(j, iv))) break;
+                        if (i + 1 < nj && !(ok = full(ik))) break;
+                        for (int w = 0; w < 2; ++w) {
+                            if (j >= e[w]) continue;
+                            if (!(ok = p_wait(w))) break;
+                            do_o(w, w, iv, i == 0);
+                            if (j + 1 < e[w]) do_s(w, w, ik);
+                            else tc_commit(&nt->o_done[w]);
+                        }
+                        tc_commit(&nt->kv_empty[iv % S::kStages]);
+                        if (i + 1 < nj) tc_commit(&nt->kv_empty[ik % S::kStages]);
+                        if (i + 2 == nj) tc_commit(&nt->q_empty);
+                    }
+                } else {
+                    for (int i = 0; i < 2 && i < nj && ok; ++i) {
+                        if (!(ok = full(it + 2 * i))) break;
+                        do_s(0, (buf + i) & 1, it + 2 * i);
+                        tc_commit(&nt->kv_empty[(it + 2 * i) % S::kStages]);
+                        if (i + 1 == nj) tc_commit(&nt->q_empty);
+                    }
+                    for (int i = 0; i < nj && ok; ++i, buf ^= 1) {
+                        const int iv = it + 2 * i + 1, ik = iv + 3;
+                        if (!(ok = v_wait(wk.j0 + i, iv)) || !(ok = p_wait(buf))) break;
+                        do_o(0, buf, iv, i == 0);
+                        tc_commit(&nt->o_done[0]);
+                        tc_commit(&nt->kv_empty[iv % S::kStages]);
+                        if (i + 2 < nj) {
+                            if (!(ok = full(ik))) break;
+                            do_s(0, buf, ik);
+                            tc_commit(&nt->kv_empty[ik % S::kStages]);
+                            if (i + 3 == nj) tc_commit(&nt->q_empty);
+                        }
+                    }
+                }
+                it += 2 * nj;
+            }
+            // no MMA of this CTA is in flight once the last commit has fired
+            tc_commit(&nt->fin);
+            tc_wait(&nt->fin, 0, a.status);
+        }
+    } else if (warp >= 10) {
+        // ---------------------------------------------------------- V tiles on the edge
+        const int x = tid - 320;                        // 0 .. 63
+        int it = 0, seg = 0, asked = 0;
+        bool ok = true;
+        while (ok && wk.next(c, a, U)) {
+            const int64_t first_pos = wk.L - wk.n + (int64_t)wk.qb * U;
+            for (int j = wk.j0; j < wk.j1; ++j, it += 2) {
+                if ((int64_t)(j + 1) * kTcTile <= first_pos + 1) continue;
+                const int s = (it + 1) % S::kStages;
+                // the issuing thread asks once the tile is in, and waits for the answer
+                ok = tc_wait(&nt->care_ask, asked & 1, a.status);
+                ++asked;
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                unsigned char* st = ring + s * S::kTileBytes;
+                const int held = (int)min((int64_t)kTcTile, wk.L - (int64_t)j * kTcTile);
+                // 16-byte chunk ch of row r sits at (ch ^ r % 8) of its 128-byte row
+                uint32_t any = 0;
+                for (int i = x; i < kTcTile * S::kHalves * 8; i += 64) {
+                    const int r = (i >> 3) & 127;
+                    uint4* p = reinterpret_cast<uint4*>(st + (i >> 10) * 16384 + (i & 1023) * 16);
+                    if (r >= held) {
+                        *p = make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        const uint4 v = *p;
+                        any |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                               ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+                    }
+                }
+                const bool found = any & 0x80008000u;
+                int some;                               // whether either warp found one
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                             "barrier.cta.red.or.pred q, 1, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                             : "=r"(some) : "r"((uint32_t)found) : "memory");
+                if (some) {
+                    if (nt->nf_seg != seg) {
+                        // the rows of the segment before have read their notes
+                        const volatile int32_t* epi = &nt->epi;
+                        const unsigned long long t1 = global_ns();
+                        while (*epi < 4 * S::kQTiles * seg && global_ns() - t1 < kTcWaitNs) {}
+                        asm volatile("bar.sync 1, 64;" ::: "memory");
+                        for (int i = x; i < 3 * 128; i += 64) nt->first[i / 128][i % 128] = 0x7fffffff;
+                        if (x == 0) nt->nf_seg = seg;
+                        asm volatile("bar.sync 1, 64;" ::: "memory");
+                    }
+                    for (int i = x; i < kTcTile * S::kHalves * 8; i += 64) {
+                        const int r = (i >> 3) & 127, pos = i & 7, hf = i >> 10;
+                        uint32_t* p = reinterpret_cast<uint32_t*>(st + hf * 16384 + (i & 1023) * 16);
+                        const int dim0 = hf * 64 + ((pos ^ (r & 7)) << 3);
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t h16 = (p[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                            if ((h16 & 0x7f80u) != 0x7f80u) continue;
+                            const int kind = (h16 & 0x7fu) ? 2 : (h16 >> 15);
+                            atomicMin(&nt->first[kind][dim0 + e], j * kTcTile + r);
+                            p[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                        }
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&nt->care_done);
+            }
+            ++seg;
+        }
+    } else if (kTwo || warp < 4) {
+        // ---------------------------------------------------------- softmax and epilogue
+        const int w = warp >> 2;                        // query tile
+        const int r = tid & 127;                        // row of the tile = TMEM lane
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;       // lane quarter, in the address
+        const uint32_t tO = tmem + 256 + 128 * w + lanes;
+        int sc = 0;                                     // steps taken (this tile's S buffers)
+        int oc = 0;                                     // o_done phases passed before this segment
+        int seg = 0;
+        bool ok = true;
+        ChunkCut cut = {};
+        while (ok && wk.next(c, a, U)) {
+            const int64_t t0 = (int64_t)wk.qb * U + w * per_tile;
+            const int tok = (int)t0 + r / G;            // query token of this row
+            const bool live = tok < wk.n;
+            const int pos = wk.L - wk.n + tok;
+            const int e = kTwo ? wk.tile_end(w, per_tile, U) : wk.j1;
+            const int lo_pos = wk.L - wk.n + (int)t0;   // of the tile's first row
+            const bool warp_live = (int)t0 + ((warp & 3) * 32) / G < wk.n;
+            float m = -SPLA_INF, l = 0.f;
+            for (int j = wk.j0; j < e; ++j, ++sc) {
+                const int buf = kTwo ? w : sc & 1;
+                const uint32_t ph = kTwo ? sc & 1 : (sc >> 1) & 1;
+                ok = tc_wait(&nt->s_full[buf], ph, a.status);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (warp_live) {
+                    tcf_after();
+                    const uint32_t tS = tmem + 128 * buf + lanes;
+                    float s[128];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tm_ld32(tS + 32 * i, s + 32 * i);
+                    tm_wait_ld<128>(s);
+                    if ((int64_t)(j + 1) * kTcTile > lo_pos + 1) {
+                        const int lim = pos - j * kTcTile;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) s[i] = i <= lim ? s[i] : -SPLA_INF;
+                    }
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int i = 4; i < 128; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = i + 4 + k < 128 ? max3(mx[k], s[i + k], s[i + 4 + k])
+                                                    : fmaxf(mx[k], s[i + k]);
+                    const float top = fmaxf(max3(mx[0], mx[1], mx[2]), fmaxf(mx[3], m));
+                    // the scale of the sums moves where there are none yet, or the maximum
+                    // has outgrown it
+                    const bool fresh = m == -SPLA_INF;
+                    const bool grow = !fresh && (top - m) * a.sl2 > kTcLazy;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? ex2((m - top) * a.sl2) : 1.f;
+                        l *= f;
+                        if (!kTwo && sc > 0 && j > wk.j0) {
+                            // the product of the step before may still be running
+                            ok = tc_wait(&nt->o_done[0], (sc - 1) & 1, a.status);
+                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                            tcf_after();
+                        }
+#pragma unroll
+                        for (int i = 0; i < D; i += 32) {
+                            float o[32];
+                            tm_ld32(tO + i, o);
+                            tm_wait_ld<32>(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] *= f;
+                            tm_st32(tO + i, reinterpret_cast<uint32_t*>(o));
+                        }
+                    }
+                    if (fresh || grow) m = top;
+                    const float m2 = m == -SPLA_INF ? 0.f : m * a.sl2;
+                    float2 sum = make_float2(0.f, 0.f), sum1 = sum;
+                    uint32_t pk[64];
+#pragma unroll
+                    for (int i = 0; i < 128; i += 4) {
+                        const float2 sl = make_float2(a.sl2, a.sl2), mm = make_float2(-m2, -m2);
+                        float2 p = fma2(make_float2(s[i], s[i + 1]), sl, mm);
+                        float2 q = fma2(make_float2(s[i + 2], s[i + 3]), sl, mm);
+                        p = make_float2(ex2(p.x), ex2(p.y));
+                        q = make_float2(ex2(q.x), ex2(q.y));
+                        sum.x += p.x;
+                        sum.y += p.y;
+                        sum1.x += q.x;
+                        sum1.y += q.y;
+                        pk[i / 2] = pack_bf16(p.x, p.y);
+                        pk[i / 2 + 1] = pack_bf16(q.x, q.y);
+                    }
+                    l += (sum.x + sum.y) + (sum1.x + sum1.y);
+                    tm_st32(tS, pk);
+                    tm_st32(tS + 32, pk + 32);
+                    tm_wait_st();
+                    tcf_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&nt->p_full[buf]);
+            }
+            if (!ok) break;
+            // ---- this segment's sums
+            const bool whole = wk.j0 == 0 && wk.j1 == wk.T;
+            const int steps = max(0, e - wk.j0);
+            if (steps > 0) {
+                const int phase = kTwo ? oc : sc - 1;
+                ok = tc_wait(&nt->o_done[w], phase & 1, a.status);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                ++oc;
+                tcf_after();
+            }
+            // a unit cut by this run's end starts a partial 1 unless it began before the run
+            const int slot = wk.j0 == 0 ? 1 : 0;
+            float* part = reinterpret_cast<float*>(a.ws + kCutBytes) +
+                          ((int64_t)blockIdx.x * 2 + slot) * part_floats(D);
+            const int row = w * 128 + r;
+            if (warp_live) {
+                const bool notes = steps > 0 && nt->nf_seg == seg;
+                const float inv = 1.f / l;
+                const int64_t orow = ((int64_t)(wk.b * (int64_t)a.max_new + tok) * c.hq +
+                                      wk.h * G + r % G);
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    float o[32];
+                    if (steps > 0) {
+                        tm_ld32(tO + i, o);
+                        tm_wait_ld<32>(o);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                    }
+                    if (notes) {
+                        for (int k = 0; k < 32; ++k) {
+                            float add = 0.f;
+                            if (nt->first[0][i + k] <= pos) add += SPLA_INF;
+                            if (nt->first[1][i + k] <= pos) add -= SPLA_INF;
+                            if (nt->first[2][i + k] <= pos) add = __int_as_float(0x7fffffff);
+                            o[k] += add;
+                        }
+                    }
+                    if (!live) continue;
+                    if (whole) {
+                        uint4* d = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + orow * D + i);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            d[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                              pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                              pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                              pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                    } else {
+                        float4* d = reinterpret_cast<float4*>(part + (int64_t)row * D + i);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+                const float m2 = m == -SPLA_INF ? -SPLA_INF : m * a.sl2;
+                if (live && whole) {
+                    if (a.lse) a.lse[orow] = (m2 + log2f(l)) * 0.69314718055994531f;
+                } else if (live) {
+                    part[256 * D + row] = m2;
+                    part[256 * D + 256 + row] = l;
+                }
+            }
+            if (wk.j0 == 0 && wk.j1 < wk.T) {
+                cut.parts = 1 + (int)((wk.T - wk.j1 + nt->run - 1) / nt->run);
+                cut.rows = (int)min((int64_t)U, wk.n - (int64_t)wk.qb * U) * G;
+                cut.b = wk.b;
+                cut.h = wk.h;
+                cut.t0 = wk.qb * U;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                __threadfence_block();
+                atomicAdd(&nt->epi, 1);
+            }
+            ++seg;
+        }
+        if (tid == 0) reinterpret_cast<ChunkCut*>(a.ws)[blockIdx.x] = cut;
+    }
+    tcf_before();
+    __syncthreads();
+    if (warp == 9) {
+        tcf_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;"
+                     :: "r"(tmem) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ the join
+// One warp per row of a unit that was cut: log-sum-exp merge of its partials in run
+// order (the result does not depend on timing), lanes over the dimensions.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
+    constexpr int CPL = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = blockIdx.y, row = blockIdx.x * kJoinWarps + warp;
+    pdl_trigger();
+    pdl_wait();
+    const ChunkCut cut = reinterpret_cast<const ChunkCut*>(a.ws)[run];
+    if (row >= cut.rows || cut.parts == 0) return;
+    const float* base = reinterpret_cast<const float*>(a.ws + kCutBytes) +
+                        (int64_t)run * 2 * part_floats(D);
+    // partial p is run + p's, slot 1 for the first of them and slot 0 after it
+    auto part = [&](int p) { return base + ((int64_t)p * 2 + (p == 0 ? 1 : 0)) * part_floats(D); };
+    float M = -SPLA_INF;
+    for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, part(p)[256 * D + row]);
+    M = warp_max(M);
+    float l = 0.f, acc[CPL] = {};
+    for (int p0 = 0; p0 < cut.parts; p0 += 32) {
+        float w = 0.f;
+        if (p0 + lane < cut.parts) {
+            const float* q = part(p0 + lane);
+            const float m = q[256 * D + row];
+            const float lp = q[256 * D + 256 + row];
+            // no tokens: no part; nothing but NaN logits: NaN
+            w = m == -SPLA_INF ? (lp == lp ? 0.f : lp) : ex2(m - M);
+            l += w * lp;
+        }
+        const int cnt = min(32, cut.parts - p0);
+        constexpr int kBatch = 4;                   // partial rows in flight
+        for (int i = 0; i < cnt; i += kBatch) {
+            float x[kBatch][CPL];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (i + u < cnt) {
+                    const float* q = part(p0 + i + u) + (int64_t)row * D + lane * CPL;
+                    if constexpr (CPL == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(q);
+                    else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(q);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float f = __shfl_sync(0xffffffffu, w, (i + u) & 31);
+                if (i + u < cnt && f != 0.f)        // a partial without tokens has no part
+#pragma unroll
+                    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
+            }
+        }
+    }
+    l = warp_sum(l);
+    const int64_t orow = ((int64_t)cut.b * a.max_new + cut.t0 + row / c.group) * c.hq +
+                         cut.h * c.group + row % c.group;
+    const float inv = 1.f / l;
+    __nv_bfloat16* o = (__nv_bfloat16*)a.out + orow * D + lane * CPL;
+    if constexpr (CPL == 4)
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                                                  pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t*>(o) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (a.lse && lane == 0) a.lse[orow] = (M + log2f(l)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host launcher
+template <int D, bool kTwo>
+static cudaError_t launch_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
+                             const CUtensorMap& tv, const ChunkArgs& a, cudaStream_t s) {
+    using S = TcShape<D, kTwo>;
+    cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<D, kTwo>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(chunk_tc_kernel<D, kTwo>, dim3(kMaxRuns), dim3(kTcThreads), S::kSmem, s, tq, tk,
+                   tv, c, a);
+    if (e != cudaSuccess) return e;
+    const int rows = (int)std::min<int64_t>(S::kRows, (int64_t)a.max_new * c.group);
+    return launch_pdl(chunk_combine_kernel<D>, dim3((rows + kJoinWarps - 1) / kJoinWarps, kMaxRuns),
+                      dim3(kJoinWarps * 32), 0, s, c, a);
+}
+
+// tq: [batch * max_new][Hq][d] with boxes of 64 dims x G heads x 128 / G tokens; tk, tv:
+// the pools as rows of d with boxes of 64 dims x 64 tokens.
+cudaError_t launch_chunk_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
+                            const CUtensorMap& tv, const ChunkArgs& a, cudaStream_t s) {
+    // two query tiles need more rows than one holds; one tile then takes half the MMAs
+    const bool two = (int64_t)a.max_new * c.group > 128;
+    if (c.d == 128)
+        return two ? launch_tc<128, true>(c, tq, tk, tv, a, s) : launch_tc<128, false>(c, tq, tk, tv, a, s);
+    return two ? launch_tc<64, true>(c, tq, tk, tv, a, s) : launch_tc<64, false>(c, tq, tk, tv, a, s);
+}
+
+}  // namespace spla
