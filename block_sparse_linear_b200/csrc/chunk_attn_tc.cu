@@ -15,8 +15,8 @@
 // chunk_combine_kernel joins.
 //
 // Warps. 0-3 and 4-7: softmax of query tile 0 and 1 (one row per thread); 8: TMA (K and V
-// tiles page by page into a ring, query tiles; no multicast); 9: issues the MMAs;
-// 10-11: look over the V tiles that some row does not see whole.
+// tiles page by page into a ring, query tiles; no multicast); 9: issues the MMAs, and
+// looks over the V tiles that some row does not see whole.
 //   S = Q K^T       M128 N128 Kd, both operands in shared memory as TMA wrote them
 //   P = exp2(sl2 S - m), rounded to bf16 over S's columns in tensor memory
 //   O += P V        M128 Nd K128, P from tensor memory, V as TMA wrote it (N-major)
@@ -44,6 +44,14 @@ namespace spla {
 constexpr int kTcThreads = 384;
 constexpr int kTcTile = 128;                 // KV tokens of a step
 constexpr int kTcSmem = 227 * 1024;
+// Registers: the kernel is launched with 168 a thread; the softmax warps (a row of logits
+// each thread) take 216 and the other four give theirs down to 72. The shares add up to
+// the launch's: 256 * 216 + 128 * 72 = 384 * 168.
+// The two sides share no code after the split, their ends included: code common to both
+// is compiled for the larger side's registers, and a warp of the smaller side that runs
+// it overwrites registers that are a softmax warp's by then.
+constexpr int kTcRegs = 168, kTcRegsMore = 216, kTcRegsLess = 72;
+static_assert(256 * kTcRegsMore + 128 * kTcRegsLess <= kTcThreads * kTcRegs, "register shares");
 constexpr float kTcLazy = 8.f;               // log2 growth of a maximum that is let stand
 
 template <int D, bool kTwo>
@@ -118,19 +126,56 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                  :: "r"(smem_u32(bar)) : "memory");
 }
 
-// 32 consecutive columns of this thread's TMEM lane; the caller waits.
+// N consecutive columns of this thread's TMEM lane, waited for: the load is asynchronous,
+// so the wait stands in the same statement and nothing can use the registers before it.
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+          "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+          "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+          "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tm_ld128(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+          "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+          "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+          "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]),
+          "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]),
+          "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+          "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]),
+          "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]),
+          "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]), "=f"(v[64]), "=f"(v[65]),
+          "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
+          "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]),
+          "=f"(v[78]), "=f"(v[79]), "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]),
+          "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]), "=f"(v[88]), "=f"(v[89]),
+          "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]),
+          "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]),
+          "=f"(v[102]), "=f"(v[103]), "=f"(v[104]), "=f"(v[105]), "=f"(v[106]), "=f"(v[107]),
+          "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]), "=f"(v[112]), "=f"(v[113]),
+          "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
+          "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]),
+          "=f"(v[126]), "=f"(v[127])
         : "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t* r) {
@@ -144,22 +189,13 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t* r) {
            "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
            "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr) : "memory");
 }
-// Waits for the loads of this thread; the values pass through, so that no use of them
-// can move above the wait.
-__device__ __forceinline__ void tm_tie(float* v) {
-    asm volatile(""
-        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-          "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
-          "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
-          "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
-          "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
-          "+f"(v[31]) :: "memory");
-}
-template <int N>
-__device__ __forceinline__ void tm_wait_ld(float* v) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; i += 32) tm_tie(v + i);
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+        :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+           "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+           "r"(r[14]), "r"(r[15]), "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -247,7 +283,7 @@ struct Walk {
 
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], care_ask, care_done, fin;
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], fin;
     int64_t scan[kTcThreads / 32];
     Walk start;
     int64_t run;                              // C
@@ -262,7 +298,8 @@ static_assert(sizeof(TcNotes) <= 2048, "control block");
 // bound is a time, looked at every 1024 polls, with a count over it.
 constexpr uint32_t kTcPolls = 1u << 28;
 constexpr unsigned long long kTcWaitNs = 5000000000ull;
-__device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     for (uint32_t i = 1; i < kTcPolls; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -271,11 +308,15 @@ __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, int32_
     set_status(status, SPLA_DEV_TIMEOUT);
     return false;
 }
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return tc_wait_long(bar, parity, status);
-}
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 template <int D, bool kTwo>
@@ -305,8 +346,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(&nt->p_full[w], 4);
             mbar_init(&nt->o_done[w], 1);
         }
-        mbar_init(&nt->care_ask, 1);
-        mbar_init(&nt->care_done, 2);
         mbar_init(&nt->fin, 1);
         fence_barrier_init();
         prefetch_tmap(&tq);
@@ -387,6 +426,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const uint32_t tmem = nt->tmem;
     Walk wk = nt->start;
 
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTcRegsLess));
     if (warp == 8) {
         // ---------------------------------------------------------- TMA producer
         int it = 0, seg = 0;                            // ring slots filled, segments
@@ -448,174 +489,159 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         if (seg > 0) mbar_wait_bounded(&nt->q_full, (seg - 1) & 1);
     } else if (warp == 9) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t kIdS = tc_idesc(128, false), kIdO = tc_idesc(D, true);
-            const uint32_t q0 = smem_u32(qtile), r0 = smem_u32(ring);
-            int it = 0, seg = 0, cares = 0;
-            int ps[2] = {0, 0};                         // probabilities taken, per buffer
-            bool ok = true;
-            auto full = [&](int i) {
-                const bool r = tc_wait(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1, a.status);
-                tcf_after();
-                return r;
-            };
-            auto do_s = [&](int w, int buf, int i) {    // S of query tile w by ring slot i
-                const uint32_t kt = r0 + (i % S::kStages) * S::kTileBytes;
-                const uint32_t qt = q0 + w * S::kTileBytes;
+        constexpr uint32_t kIdS = tc_idesc(128, false), kIdO = tc_idesc(D, true);
+        const uint32_t q0 = smem_u32(qtile), r0 = smem_u32(ring);
+        int it = 0, seg = 0;
+        int ps[2] = {0, 0};                             // probabilities taken, per buffer
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool r = __all_sync(0xffffffffu, tc_wait(bar, parity, a.status));
+            tcf_after();
+            return r;
+        };
+        auto full = [&](int i) { return wait(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1); };
+        auto commit = [&](uint64_t* bar) {
+            if (lane == 0) tc_commit(bar);
+        };
+        auto do_s = [&](int w, int buf, int i) {        // S of query tile w by ring slot i
+            if (lane == 0) {
+                const uint64_t kd = tc_desc(r0 + (i % S::kStages) * S::kTileBytes, 16);
+                const uint64_t qd = tc_desc(q0 + w * S::kTileBytes, 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
-                    mma_ss(tmem + 128 * buf, tc_desc(qt + off, 16), tc_desc(kt + off, 16), kIdS,
-                           kk != 0);
+                    const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+                    mma_ss(tmem + 128 * buf, qd + off, kd + off, kIdS, kk != 0);
                 }
                 tc_commit(&nt->s_full[buf]);
-            };
-            auto do_o = [&](int w, int buf, int i, bool first) {
-                const uint32_t vt = r0 + (i % S::kStages) * S::kTileBytes;
+            }
+        };
+        auto do_o = [&](int w, int buf, int i, bool first) {
+            if (lane == 0) {
+                const uint64_t vd = tc_desc(r0 + (i % S::kStages) * S::kTileBytes, 16384);
 #pragma unroll
                 for (int kk = 0; kk < kTcTile / 16; ++kk)
-                    mma_ts(tmem + 256 + 128 * w, tmem + 128 * buf + 8 * kk,
-                           tc_desc(vt + kk * 2048, 16384), kIdO, !first || kk != 0);
-            };
-            auto p_wait = [&](int buf) {
-                const bool r = tc_wait(&nt->p_full[buf], ps[buf] & 1, a.status);
-                ++ps[buf];
-                tcf_after();
-                return r;
-            };
-            auto v_wait = [&](int j, int i) {           // V of step j is in and looked over
-                if (!full(i)) return false;
-                if ((int64_t)(j + 1) * kTcTile > wk.L - wk.n + (int64_t)wk.qb * U + 1) {
-                    mbar_arrive(&nt->care_ask);
-                    const bool r = tc_wait(&nt->care_done, cares & 1, a.status);
-                    ++cares;
-                    tcf_after();
-                    return r;
-                }
-                return true;
-            };
-            int buf = 0;                                // S buffer of the next step (one tile)
-            while (ok && wk.next(c, a, U)) {
-                ok = tc_wait(&nt->q_full, seg & 1, a.status);
-                if (!ok) break;
-                ++seg;
-                tcf_after();
-                const int nj = wk.j1 - wk.j0;
-                if constexpr (kTwo) {
-                    const int e[2] = {wk.tile_end(0, per_tile, U), wk.tile_end(1, per_tile, U)};
-                    // slot it + 2 i is K of step i, it + 2 i + 1 its V
-                    if (!(ok = full(it))) break;
-                    for (int w = 0; w < 2; ++w)
-                        if (wk.j0 < e[w]) do_s(w, w, it);
-                    tc_commit(&nt->kv_empty[it % S::kStages]);
-                    if (nj == 1) tc_commit(&nt->q_empty);
-                    for (int i = 0; i < nj && ok; ++i) {
-                        const int j = wk.j0 + i, iv = it + 2 * i + 1, ik = iv + 1;
-                        if (!(ok = v_wait(j, iv))) break;
-                        if (i + 1 < nj && !(ok = full(ik))) break;
-                        for (int w = 0; w < 2; ++w) {
-                            if (j >= e[w]) continue;
-                            if (!(ok = p_wait(w))) break;
-                            do_o(w, w, iv, i == 0);
-                            if (j + 1 < e[w]) do_s(w, w, ik);
-                            else tc_commit(&nt->o_done[w]);
-                        }
-                        tc_commit(&nt->kv_empty[iv % S::kStages]);
-                        if (i + 1 < nj) tc_commit(&nt->kv_empty[ik % S::kStages]);
-                        if (i + 2 == nj) tc_commit(&nt->q_empty);
-                    }
-                } else {
-                    for (int i = 0; i < 2 && i < nj && ok; ++i) {
-                        if (!(ok = full(it + 2 * i))) break;
-                        do_s(0, (buf + i) & 1, it + 2 * i);
-                        tc_commit(&nt->kv_empty[(it + 2 * i) % S::kStages]);
-                        if (i + 1 == nj) tc_commit(&nt->q_empty);
-                    }
-                    for (int i = 0; i < nj && ok; ++i, buf ^= 1) {
-                        const int iv = it + 2 * i + 1, ik = iv + 3;
-                        if (!(ok = v_wait(wk.j0 + i, iv)) || !(ok = p_wait(buf))) break;
-                        do_o(0, buf, iv, i == 0);
-                        tc_commit(&nt->o_done[0]);
-                        tc_commit(&nt->kv_empty[iv % S::kStages]);
-                        if (i + 2 < nj) {
-                            if (!(ok = full(ik))) break;
-                            do_s(0, buf, ik);
-                            tc_commit(&nt->kv_empty[ik % S::kStages]);
-                            if (i + 3 == nj) tc_commit(&nt->q_empty);
-                        }
-                    }
-                }
-                it += 2 * nj;
+                    mma_ts(tmem + 256 + 128 * w, tmem + 128 * buf + 8 * kk, vd + kk * (2048 >> 4),
+                           kIdO, !first || kk != 0);
             }
-            // no MMA of this CTA is in flight once the last commit has fired
-            tc_commit(&nt->fin);
-            tc_wait(&nt->fin, 0, a.status);
-        }
-    } else if (warp >= 10) {
-        // ---------------------------------------------------------- V tiles on the edge
-        const int x = tid - 320;                        // 0 .. 63
-        int it = 0, seg = 0, asked = 0;
-        bool ok = true;
+        };
+        auto p_wait = [&](int buf) {
+            const bool r = wait(&nt->p_full[buf], ps[buf] & 1);
+            ++ps[buf];
+            return r;
+        };
+        // V of step j is in; where some row does not see all of it, its rows past the
+        // sequence are zeroed and its infinities and NaN noted and taken out. The softmax of
+        // the step runs meanwhile.
+        auto v_wait = [&](int j, int i) {
+            if (!full(i)) return false;
+            if ((int64_t)(j + 1) * kTcTile <= wk.L - wk.n + (int64_t)wk.qb * U + 1) return true;
+            unsigned char* st = ring + (i % S::kStages) * S::kTileBytes;
+            const int held = (int)min((int64_t)kTcTile, wk.L - (int64_t)j * kTcTile);
+            uint32_t any = 0;
+#pragma unroll 8
+            for (int x = lane; x < kTcTile * S::kHalves * 8; x += 32) {
+                uint4* p = reinterpret_cast<uint4*>(st) + x;
+                if (((x >> 3) & 127) >= held) {
+                    *p = make_uint4(0u, 0u, 0u, 0u);
+                } else {                                // an exponent of all ones carries out
+                    const uint4 v = *p;
+                    any |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                           ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+                }
+            }
+            if (__any_sync(0xffffffffu, any & 0x80008000u)) {
+                if (nt->nf_seg != seg) {
+                    // the rows of the segments before have read their notes
+                    const volatile int32_t* epi = &nt->epi;
+                    const unsigned long long t1 = global_ns();
+                    while (*epi < 4 * S::kQTiles * seg && global_ns() - t1 < kTcWaitNs) {}
+                    __syncwarp();
+                    for (int x = lane; x < 3 * 128; x += 32) nt->first[x / 128][x % 128] = 0x7fffffff;
+                    if (lane == 0) nt->nf_seg = seg;
+                    __syncwarp();
+                }
+                // 16-byte chunk ch of row r sits at position ch ^ (r % 8) of its 128-byte row
+                for (int x = lane; x < kTcTile * S::kHalves * 8; x += 32) {
+                    const int r = (x >> 3) & 127, dim0 = (x >> 10) * 64 + (((x & 7) ^ (r & 7)) << 3);
+                    uint32_t* p = reinterpret_cast<uint32_t*>(st + x * 16);
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t h16 = (p[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                        if ((h16 & 0x7f80u) != 0x7f80u) continue;
+                        const int kind = (h16 & 0x7fu) ? 2 : (h16 >> 15);
+                        atomicMin(&nt->first[kind][dim0 + e], j * kTcTile + r);
+                        p[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                    }
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            return true;
+        };
+        int buf = 0;                                    // S buffer of the next step (one tile)
         while (ok && wk.next(c, a, U)) {
-            const int64_t first_pos = wk.L - wk.n + (int64_t)wk.qb * U;
-            for (int j = wk.j0; j < wk.j1; ++j, it += 2) {
-                if ((int64_t)(j + 1) * kTcTile <= first_pos + 1) continue;
-                const int s = (it + 1) % S::kStages;
-                // the issuing thread asks once the tile is in, and waits for the answer
-                ok = tc_wait(&nt->care_ask, asked & 1, a.status);
-                ++asked;
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                unsigned char* st = ring + s * S::kTileBytes;
-                const int held = (int)min((int64_t)kTcTile, wk.L - (int64_t)j * kTcTile);
-                // 16-byte chunk ch of row r sits at (ch ^ r % 8) of its 128-byte row
-                uint32_t any = 0;
-                for (int i = x; i < kTcTile * S::kHalves * 8; i += 64) {
-                    const int r = (i >> 3) & 127;
-                    uint4* p = reinterpret_cast<uint4*>(st + (i >> 10) * 16384 + (i & 1023) * 16);
-                    if (r >= held) {
-                        *p = make_uint4(0u, 0u, 0u, 0u);
-                    } else {
-                        const uint4 v = *p;
-                        any |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                               ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+            if (!(ok = wait(&nt->q_full, seg & 1))) break;
+            const int nj = wk.j1 - wk.j0;
+            if constexpr (kTwo) {
+                const int e[2] = {wk.tile_end(0, per_tile, U), wk.tile_end(1, per_tile, U)};
+                // slot it + 2 i is K of step i, it + 2 i + 1 its V
+                if (!(ok = full(it))) break;
+                for (int w = 0; w < 2; ++w)
+                    if (wk.j0 < e[w]) do_s(w, w, it);
+                commit(&nt->kv_empty[it % S::kStages]);
+                if (nj == 1) commit(&nt->q_empty);
+                for (int i = 0; i < nj && ok; ++i) {
+                    const int j = wk.j0 + i, iv = it + 2 * i + 1, ik = iv + 1;
+                    if (!(ok = v_wait(j, iv))) break;
+                    if (i + 1 < nj && !(ok = full(ik))) break;
+                    for (int w = 0; w < 2; ++w) {
+                        if (j >= e[w]) continue;
+                        if (!(ok = p_wait(w))) break;
+                        do_o(w, w, iv, i == 0);
+                        if (j + 1 < e[w]) do_s(w, w, ik);
+                        else commit(&nt->o_done[w]);
+                    }
+                    commit(&nt->kv_empty[iv % S::kStages]);
+                    if (i + 1 < nj) commit(&nt->kv_empty[ik % S::kStages]);
+                    if (i + 2 == nj) commit(&nt->q_empty);
+                }
+            } else {
+                for (int i = 0; i < 2 && i < nj && ok; ++i) {
+                    if (!(ok = full(it + 2 * i))) break;
+                    do_s(0, (buf + i) & 1, it + 2 * i);
+                    commit(&nt->kv_empty[(it + 2 * i) % S::kStages]);
+                    if (i + 1 == nj) commit(&nt->q_empty);
+                }
+                for (int i = 0; i < nj && ok; ++i, buf ^= 1) {
+                    const int iv = it + 2 * i + 1, ik = iv + 3;
+                    if (!(ok = v_wait(wk.j0 + i, iv)) || !(ok = p_wait(buf))) break;
+                    do_o(0, buf, iv, i == 0);
+                    commit(&nt->o_done[buf]);
+                    commit(&nt->kv_empty[iv % S::kStages]);
+                    if (i + 2 < nj) {
+                        if (!(ok = full(ik))) break;
+                        do_s(0, buf, ik);
+                        commit(&nt->kv_empty[ik % S::kStages]);
+                        if (i + 3 == nj) commit(&nt->q_empty);
                     }
                 }
-                const bool found = any & 0x80008000u;
-                int some;                               // whether either warp found one
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                             "barrier.cta.red.or.pred q, 1, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                             : "=r"(some) : "r"((uint32_t)found) : "memory");
-                if (some) {
-                    if (nt->nf_seg != seg) {
-                        // the rows of the segment before have read their notes
-                        const volatile int32_t* epi = &nt->epi;
-                        const unsigned long long t1 = global_ns();
-                        while (*epi < 4 * S::kQTiles * seg && global_ns() - t1 < kTcWaitNs) {}
-                        asm volatile("bar.sync 1, 64;" ::: "memory");
-                        for (int i = x; i < 3 * 128; i += 64) nt->first[i / 128][i % 128] = 0x7fffffff;
-                        if (x == 0) nt->nf_seg = seg;
-                        asm volatile("bar.sync 1, 64;" ::: "memory");
-                    }
-                    for (int i = x; i < kTcTile * S::kHalves * 8; i += 64) {
-                        const int r = (i >> 3) & 127, pos = i & 7, hf = i >> 10;
-                        uint32_t* p = reinterpret_cast<uint32_t*>(st + hf * 16384 + (i & 1023) * 16);
-                        const int dim0 = hf * 64 + ((pos ^ (r & 7)) << 3);
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t h16 = (p[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                            if ((h16 & 0x7f80u) != 0x7f80u) continue;
-                            const int kind = (h16 & 0x7fu) ? 2 : (h16 >> 15);
-                            atomicMin(&nt->first[kind][dim0 + e], j * kTcTile + r);
-                            p[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
-                        }
-                    }
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&nt->care_done);
             }
+            it += 2 * nj;
             ++seg;
         }
-    } else if (kTwo || warp < 4) {
+        // no MMA of this CTA is in flight once the last commit has fired
+        commit(&nt->fin);
+        tc_wait(&nt->fin, 0, a.status);
+    }
+    tcf_before();
+    asm volatile("bar.sync 1, %0;" :: "n"(kTcThreads) : "memory");
+    if (warp == 9) {
+        tcf_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;"
+                     :: "r"(tmem) : "memory");
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kTcRegsMore));
+    if (kTwo || warp < 4) {
         // ---------------------------------------------------------- softmax and epilogue
         const int w = warp >> 2;                        // query tile
         const int r = tid & 127;                        // row of the tile = TMEM lane
@@ -644,9 +670,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     tcf_after();
                     const uint32_t tS = tmem + 128 * buf + lanes;
                     float s[128];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tm_ld32(tS + 32 * i, s + 32 * i);
-                    tm_wait_ld<128>(s);
+                    tm_ld128(tS, s);
                     if ((int64_t)(j + 1) * kTcTile > lo_pos + 1) {
                         const int lim = pos - j * kTcTile;
 #pragma unroll
@@ -669,7 +693,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         l *= f;
                         if (!kTwo && sc > 0 && j > wk.j0) {
                             // the product of the step before may still be running
-                            ok = tc_wait(&nt->o_done[0], (sc - 1) & 1, a.status);
+                            ok = tc_wait(&nt->o_done[(sc - 1) & 1], ((sc - 1) >> 1) & 1, a.status);
                             if (!(ok = __all_sync(0xffffffffu, ok))) break;
                             tcf_after();
                         }
@@ -677,7 +701,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         for (int i = 0; i < D; i += 32) {
                             float o[32];
                             tm_ld32(tO + i, o);
-                            tm_wait_ld<32>(o);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) o[k] *= f;
                             tm_st32(tO + i, reinterpret_cast<uint32_t*>(o));
@@ -685,25 +708,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     }
                     if (fresh || grow) m = top;
                     const float m2 = m == -SPLA_INF ? 0.f : m * a.sl2;
+                    const float2 sl = make_float2(a.sl2, a.sl2), mm = make_float2(-m2, -m2);
                     float2 sum = make_float2(0.f, 0.f), sum1 = sum;
-                    uint32_t pk[64];
 #pragma unroll
-                    for (int i = 0; i < 128; i += 4) {
-                        const float2 sl = make_float2(a.sl2, a.sl2), mm = make_float2(-m2, -m2);
-                        float2 p = fma2(make_float2(s[i], s[i + 1]), sl, mm);
-                        float2 q = fma2(make_float2(s[i + 2], s[i + 3]), sl, mm);
-                        p = make_float2(ex2(p.x), ex2(p.y));
-                        q = make_float2(ex2(q.x), ex2(q.y));
-                        sum.x += p.x;
-                        sum.y += p.y;
-                        sum1.x += q.x;
-                        sum1.y += q.y;
-                        pk[i / 2] = pack_bf16(p.x, p.y);
-                        pk[i / 2 + 1] = pack_bf16(q.x, q.y);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float2 p = fma2(make_float2(s[32 * k + i], s[32 * k + i + 1]), sl, mm);
+                            float2 q = fma2(make_float2(s[32 * k + i + 2], s[32 * k + i + 3]), sl, mm);
+                            p = make_float2(ex2(p.x), ex2(p.y));
+                            q = make_float2(ex2(q.x), ex2(q.y));
+                            sum = add2(sum, p);
+                            sum1 = add2(sum1, q);
+                            pk[i / 2] = pack_bf16(p.x, p.y);
+                            pk[i / 2 + 1] = pack_bf16(q.x, q.y);
+                        }
+                        tm_st16(tS + 16 * k, pk);
                     }
                     l += (sum.x + sum.y) + (sum1.x + sum1.y);
-                    tm_st32(tS, pk);
-                    tm_st32(tS + 32, pk + 32);
                     tm_wait_st();
                     tcf_before();
                 }
@@ -715,8 +738,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const bool whole = wk.j0 == 0 && wk.j1 == wk.T;
             const int steps = max(0, e - wk.j0);
             if (steps > 0) {
-                const int phase = kTwo ? oc : sc - 1;
-                ok = tc_wait(&nt->o_done[w], phase & 1, a.status);
+                // one tile: the products alternate between two barriers, since the one before
+                // the last may still be running here (never more: the last S was issued
+                // after the product two steps back)
+                ok = kTwo ? tc_wait(&nt->o_done[w], oc & 1, a.status)
+                          : tc_wait(&nt->o_done[(sc - 1) & 1], ((sc - 1) >> 1) & 1, a.status);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ++oc;
                 tcf_after();
@@ -736,7 +762,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     float o[32];
                     if (steps > 0) {
                         tm_ld32(tO + i, o);
-                        tm_wait_ld<32>(o);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = 0.f;
@@ -750,8 +775,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                             o[k] += add;
                         }
                     }
-                    if (!live) continue;
-                    if (whole) {
+                    if (live && whole) {
                         uint4* d = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + orow * D + i);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -759,12 +783,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                                               pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
                                               pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
                                               pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                    } else {
+                    } else if (live) {
                         float4* d = reinterpret_cast<float4*>(part + (int64_t)row * D + i);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
+                    __syncwarp();                       // the next load is the whole warp's
                 }
                 const float m2 = m == -SPLA_INF ? -SPLA_INF : m * a.sl2;
                 if (live && whole) {
@@ -791,11 +816,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         if (tid == 0) reinterpret_cast<ChunkCut*>(a.ws)[blockIdx.x] = cut;
     }
     tcf_before();
-    __syncthreads();
-    if (warp == 9) {
-        tcf_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;"
-                     :: "r"(tmem) : "memory");
+    asm volatile("bar.sync 1, %0;" :: "n"(kTcThreads) : "memory");
     }
 }
 
