@@ -98,9 +98,21 @@ __device__ __forceinline__ void tcf_after() {
 // Shared-memory matrix descriptors, 128-byte swizzle, 1024-byte aligned 8-row atoms
 // (version 1). K-major: rows of 64 elements, 8-row groups 1024 bytes apart. MN-major:
 // 64-element atoms `lbo` bytes apart, 8-row groups of K 1024 bytes apart.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-           (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// The words: address and lbo in units of 16 bytes; the rest is constant.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t tc_desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ uint64_t tc_desc(uint32_t lo) {
+    return (uint64_t)kDescHi << 32 | lo;
+}
+
+// One thread of the converged warp; the others skip what it guards.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
 // kind::f16, fp32 accumulator, bf16 operands, A K-major, M = 128.
@@ -500,28 +512,35 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             return r;
         };
         auto full = [&](int i) { return wait(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1); };
+        // Descriptor words and addresses are made by the whole warp from lane 0's values, so
+        // that they stand in uniform registers where the MMAs want them: made within the
+        // elected thread's branch, each MMA took twice as long to issue as to run.
+        auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
         auto commit = [&](uint64_t* bar) {
-            if (lane == 0) tc_commit(bar);
+            if (elect_one()) tc_commit(bar);
         };
         auto do_s = [&](int w, int buf, int i) {        // S of query tile w by ring slot i
-            if (lane == 0) {
-                const uint64_t kd = tc_desc(r0 + (i % S::kStages) * S::kTileBytes, 16);
-                const uint64_t qd = tc_desc(q0 + w * S::kTileBytes, 16);
+            const uint32_t kd = uni(tc_desc_lo(r0 + (i % S::kStages) * S::kTileBytes, 16));
+            const uint32_t qd = uni(tc_desc_lo(q0 + w * S::kTileBytes, 16));
+            const uint32_t dst = uni(tmem + 128 * buf);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-                    mma_ss(tmem + 128 * buf, qd + off, kd + off, kIdS, kk != 0);
+                    mma_ss(dst, tc_desc(qd + off), tc_desc(kd + off), kIdS, kk != 0);
                 }
                 tc_commit(&nt->s_full[buf]);
             }
         };
         auto do_o = [&](int w, int buf, int i, bool first) {
-            if (lane == 0) {
-                const uint64_t vd = tc_desc(r0 + (i % S::kStages) * S::kTileBytes, 16384);
+            const uint32_t vd = uni(tc_desc_lo(r0 + (i % S::kStages) * S::kTileBytes, 16384));
+            const uint32_t dst = uni(tmem + 256 + 128 * w), src = uni(tmem + 128 * buf);
+            const uint32_t acc = uni(first ? 0u : 1u);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTcTile / 16; ++kk)
-                    mma_ts(tmem + 256 + 128 * w, tmem + 128 * buf + 8 * kk, vd + kk * (2048 >> 4),
-                           kIdO, !first || kk != 0);
+                    mma_ts(dst, src + 8 * kk, tc_desc(vd + kk * (2048 >> 4)), kIdO,
+                           kk != 0 ? 1u : acc);
             }
         };
         auto p_wait = [&](int buf) {
