@@ -58,8 +58,8 @@ cudaError_t launch_block_plan(const spla_block_pool* pool, const int32_t* lens,
 cudaError_t launch_block_release(const spla_block_pool* pool, const int32_t* keep_lens,
                                  int32_t* lens, int32_t* status, cudaStream_t s);
 cudaError_t launch_norm_rope(const RopeArgs& a, int d, int dtype, cudaStream_t s);
-size_t chunk_workspace_bytes(int d, int dtype);
-cudaError_t launch_chunk_simt(const CacheView& c, int dtype, const ChunkArgs& a, cudaStream_t s);
+size_t chunk_workspace_bytes(int d);
+cudaError_t launch_chunk_f32(const CacheView& c, const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const ChunkArgs& a, cudaStream_t s);
 
@@ -788,7 +788,7 @@ spla_status spla_chunk_attention_workspace_size(const spla_params* params, int32
     spla_status st = check_chunk(params, batch, max_new);
     if (st != SPLA_OK) return st;
     if (!bytes) return SPLA_ERR_INVALID_ARG;
-    *bytes = chunk_workspace_bytes(params->head_dim, params->dtype);
+    *bytes = chunk_workspace_bytes(params->head_dim);
     return SPLA_OK;
 }
 
@@ -814,7 +814,7 @@ spla_status spla_chunk_attention(const spla_params* params, const spla_cache* ca
     const uint64_t qn = (uint64_t)v.batch * max_new * v.hq * v.d *
                         (params->dtype == SPLA_BF16 ? 2 : 4);
     if (overlap(q, qn, out, qn)) return SPLA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < chunk_workspace_bytes(v.d, params->dtype) ||
+    if (!workspace || workspace_bytes < chunk_workspace_bytes(v.d) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255))
         return SPLA_ERR_WORKSPACE;
     const double scale = params->softmax_scale > 0.f ? (double)params->softmax_scale
@@ -836,7 +836,7 @@ spla_status spla_chunk_attention(const spla_params* params, const spla_cache* ca
             return cuda_fail(cudaErrorInvalidValue);
         e = launch_chunk_tc(v, tq, tk, tv, a, (cudaStream_t)stream);
     } else {
-        e = launch_chunk_simt(v, params->dtype, a, (cudaStream_t)stream);
+        e = launch_chunk_f32(v, a, (cudaStream_t)stream);
     }
     return e == cudaSuccess ? SPLA_OK : cuda_fail(e);
 }

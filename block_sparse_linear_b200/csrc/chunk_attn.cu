@@ -1,106 +1,429 @@
-// Exact causal attention of a chunk of new tokens over the paged cache. With L_b tokens
-// held by sequence b, the chunk's n_b among them, query t of the chunk stands at
-// position L_b - n_b + t and sees the tokens up to its own:
-//   o_t = sum_{s <= pos_t} p_ts v_s / sum p_ts,   p_ts = exp(scale q_t . k_s),
-//   lse_t = log sum_{s <= pos_t} p_ts
-// in one pass over the tokens with a running maximum (softmax attention as in the Baidu
-// article's section 1; the paged pools are the decode path's own).
-#include "common.cuh"
+// Chunk attention, fp32, and the join of both types' partials. chunk_attn.cuh states the
+// mathematics and the split over the GPU.
+//
+// The products run on the tensor cores in three parts: x = hi + lo with hi the tf32 part
+// of x (its upper 11 significant bits) and lo the exact rest, rounded to tf32, and
+// a b = hi hi + hi lo + lo hi. What is dropped, lo lo, and the rounding of lo are 2^-22 of
+// a product, as fp32's own rounding is 2^-24 of a sum: the results are fp32 attention's
+// (tensor cores take tf32 at most, and fp32 FMAs have a quarter of this rate). mma.sync
+// m16n8k8 with the operands split in registers: the split parts of a tile would take twice
+// the shared memory, and these sizes are bound by the split's own instructions and by
+// shared-memory loads, not by the tensor pipe that tcgen05 would widen.
+//
+// A CTA of 8 warps: WM of them side by side over rows (16 each), 8 / WM over the tokens of
+// a 64-token step, chosen so that few rows (decode) still use every warp; their sums meet
+// in shared memory at the end of a segment. K and V tiles come through cp.async into a
+// two-stage ring, rows padded by 16 bytes (every fragment load is free of bank conflicts).
+// The probabilities' accumulator layout is the next product's A layout once the tokens of
+// a group of 8 are taken in the order 0 2 4 6 1 3 5 7, which the V loads follow.
+//
+// Infinities and NaN in V: a probability of zero does not cancel them and the split turns
+// an infinity into NaN, so they are taken out of each tile and noted (first token per
+// dimension and kind), and the epilogue adds them to the rows that see that token.
+#include <algorithm>
+
+#include "chunk_attn.cuh"
 
 namespace spla {
 
-// The chunk of sequence b: false (and a status bit) where its count or length is out of range.
-__device__ __forceinline__ bool chunk_of(const CacheView& c, const ChunkArgs& a, int b,
-                                         int32_t* L, int32_t* n, bool flag) {
-    *L = c.lens[b];
-    *n = a.n_new[b];
-    int32_t bad = 0;
-    if (*n < 0 || *n > a.max_new) bad = SPLA_DEV_BAD_COUNT;
-    else if (*L < 0 || *L > (int64_t)c.mbp * c.bs) bad = SPLA_DEV_CAPACITY;
-    else if (*n > *L) bad = SPLA_DEV_BAD_COUNT;
-    if (bad && flag) set_status(a.status, bad);
-    return bad == 0;
+constexpr int kFKT = 64;                            // tokens of a step
+constexpr int kFThreads = 256;
+using FWalk = Walk<kFKT>;
+
+template <int D>
+struct FShape {
+    static constexpr int kLd = D + 4;               // floats between tile rows
+    static constexpr int kTile = kFKT * kLd;
+    static constexpr size_t kSmem = (size_t)4 * kTile * sizeof(float);
+    static_assert(128 * kLd + 256 <= 4 * kTile, "the warps' sums fit where the tiles were");
+};
+
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;    // rounded where the MMA cuts it
+}
+// D += A (16x8, row) * B (8x8, col), tf32.
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_3tf32(float* c, const uint32_t* ah, const uint32_t* al,
+                                          float b0, float b1) {
+    uint32_t h0, l0, h1, l1;
+    split_tf32(b0, h0, l0);
+    split_tf32(b1, h1, l1);
+    mma_tf32(c, al, h0, h1);
+    mma_tf32(c, ah, l0, l1);
+    mma_tf32(c, ah, h0, h1);
 }
 
-constexpr int kSimtWarps = 4;
-
-// One warp per (sequence, new token, query head): lanes over 32 tokens for the logits,
-// over dimensions for the values.
-template <int D, typename T>
-__global__ void __launch_bounds__(kSimtWarps * 32)
-chunk_simt_kernel(CacheView c, ChunkArgs a) {
-    __shared__ float qs[kSimtWarps][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <int D, int WM>
+__global__ void __launch_bounds__(kFThreads, 1)
+chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
+    using S = FShape<D>;
+    constexpr int WN = 8 / WM, NT = 8 / WN;         // token groups of 8 per warp and step
+    constexpr int kRows = 16 * WM;
+    extern __shared__ __align__(16) float f_smem[];
+    __shared__ int64_t scan[kFThreads / 32], run;
+    __shared__ FWalk start;
+    __shared__ int32_t first[3][D], noted;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wm = warp % WM, wn = warp / WM, g = lane >> 2, t = lane & 3;
+    const int G = c.group, U = kRows / G;
+    if (tid == 0) start.left = 0;
     pdl_trigger();
     pdl_wait();
-    const int64_t row = (int64_t)blockIdx.x * kSimtWarps + warp;
-    if (row >= (int64_t)c.batch * a.max_new * c.hq) return;
-    const int hq = (int)(row % c.hq);
-    const int64_t bt = row / c.hq;
-    const int b = (int)(bt / a.max_new), t = (int)(bt - (int64_t)b * a.max_new);
-    int32_t L, n;
-    if (!chunk_of(c, a, b, &L, &n, t == 0 && hq == 0 && lane == 0) || t >= n) return;
-    const int h = hq / c.group;
-    const T* q = (const T*)a.q + row * D;
-    for (int i = lane; i < D; i += 32) qs[warp][i] = to_f<T>(q[i]) * a.sl2;
-    __syncwarp();
-    const int pos = L - n + t;
-    float m = -SPLA_INF, l = 0.f;
-    constexpr int CPL = D / 32;
-    float acc[CPL] = {};
-    for (int s0 = 0; s0 <= pos; s0 += 32) {
-        const int s = s0 + lane;
-        const int lb = s0 / c.bs;                 // 32 divides the block size
-        const int32_t phys = c.table[(int64_t)b * c.mbp + lb];
-        const bool good = phys >= 0 && phys < c.num_phys;
-        if (!good && lane == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
-        const int64_t base = (((int64_t)(good ? phys : 0) * c.hkv + h) * c.bs + (s0 - lb * c.bs)) * D;
-        float x = -SPLA_INF;
-        if (s <= pos) {
-            x = 0.f;
-            const T* k = (const T*)c.k_pool + base + (int64_t)lane * D;
-            if (good)
-                for (int i = 0; i < D; ++i) x = fmaf(qs[warp][i], to_f<T>(k[i]), x);
+    find_run<kFKT, kFThreads>(c, a, U, scan, &start, &run);
+    FWalk wk = start;
+    ChunkCut cut = {};
+    auto ktile = [&](int s) { return f_smem + s * 2 * S::kTile; };
+    auto vtile = [&](int s) { return f_smem + s * 2 * S::kTile + S::kTile; };
+
+    while (wk.next(c, a, U)) {
+        const int tok0 = wk.qb * U;
+        const int base_pos = wk.L - wk.n;
+        // this lane's two rows
+        const int row_a = wm * 16 + g, row_b = row_a + 8;
+        const int tok_a = tok0 + row_a / G, tok_b = tok0 + row_b / G;
+        const int pos_a = base_pos + tok_a, pos_b = base_pos + tok_b;
+        const bool warp_live = tok0 + wm * 16 / G < wk.n;
+        float q[D / 8][4];
+        {
+            const float* qp = (const float*)a.q + ((int64_t)wk.b * a.max_new * c.hq + wk.h * G) * D;
+            const float* qa = qp + ((int64_t)tok_a * c.hq + row_a % G) * D + t;
+            const float* qb = qp + ((int64_t)tok_b * c.hq + row_b % G) * D + t;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+                q[k][0] = tok_a < wk.n ? qa[8 * k] : 0.f;
+                q[k][1] = tok_b < wk.n ? qb[8 * k] : 0.f;
+                q[k][2] = tok_a < wk.n ? qa[8 * k + 4] : 0.f;
+                q[k][3] = tok_b < wk.n ? qb[8 * k + 4] : 0.f;
+            }
         }
-        const float mn = fmaxf(m, warp_max(x));
-        const float mu = mn == -SPLA_INF ? 0.f : mn;
-        const float f = exp2f(m - mu);
-        const float p = exp2f(x - mu);
-        l = l * f + warp_sum(p);
-        m = mn;
+        float o[D / 8][4] = {};
+        float m_a = -SPLA_INF, m_b = -SPLA_INF, l_a = 0.f, l_b = 0.f;
+        __syncthreads();                            // the last segment's sums have been read
+        for (int i = tid; i < 3 * D; i += kFThreads) first[i / D][i % D] = 0x7fffffff;
+        if (tid == 0) noted = 0;
+
+        const int32_t* table = c.table + (int64_t)wk.b * c.mbp;
+        auto load = [&](int j, int s) {             // a step's tiles; slots past the end are zeros
+            const int lb = j * kFKT / c.bs;
+            const int32_t phys = table[lb];
+            const bool good = phys >= 0 && phys < c.num_phys;
+            if (!good && tid == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
+            const int64_t at = (((int64_t)(good ? phys : 0) * c.hkv + wk.h) * c.bs +
+                                (j * kFKT - lb * c.bs)) * D;
+            const int held = good ? min(kFKT, wk.L - j * kFKT) : 0;
+            for (int i = tid; i < kFKT * (D / 4); i += kFThreads) {
+                const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+                const int64_t src = at + (r < held ? (int64_t)r * D + x : 0);
+                cp_async16(ktile(s) + r * S::kLd + x, (const float*)c.k_pool + src, r < held);
+                cp_async16(vtile(s) + r * S::kLd + x, (const float*)c.v_pool + src, r < held);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        __syncthreads();
+        load(wk.j0, 0);
+        for (int j = wk.j0; j < wk.j1; ++j) {
+            const int s = (j - wk.j0) & 1;
+            if (j + 1 < wk.j1) {
+                load(j + 1, s ^ 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            // the chunks of V this thread fetched
+            for (int i = tid; i < kFKT * (D / 4); i += kFThreads) {
+                const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+                float* p = vtile(s) + r * S::kLd + x;
+                const float4 v = *reinterpret_cast<const float4*>(p);
+                const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+                // (a maximum passes over NaN: the sum of zero products does not)
+                if (!(big < SPLA_INF) || !((v.x * 0.f + v.y * 0.f) + (v.z * 0.f + v.w * 0.f) == 0.f)) {
+                    for (int e = 0; e < 4; ++e)
+                        if (!(fabsf(p[e]) < SPLA_INF)) {
+                            const int kind = p[e] != p[e] ? 2 : p[e] < 0.f;
+                            atomicMin(&first[kind][x + e], j * kFKT + r);
+                            p[e] = 0.f;
+                            noted = 1;
+                        }
+                }
+            }
+            __syncthreads();
+            if (warp_live) {
+                const float* kt = ktile(s) + (wn * NT * 8) * S::kLd;
+                const float* vt = vtile(s) + (wn * NT * 8) * S::kLd;
+                float x[NT][4] = {};
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) acc[i] *= f;
-        const int cnt = min(32, pos - s0 + 1);
-        const T* v = (const T*)c.v_pool + base + lane * CPL;
-        for (int j = 0; j < cnt; ++j) {
-            const float pj = __shfl_sync(0xffffffffu, p, j);
-            if (good)
+                for (int k = 0; k < D / 8; ++k) {
+                    uint32_t ah[4], al[4];
 #pragma unroll
-                for (int i = 0; i < CPL; ++i)
-                    acc[i] = fmaf(pj, to_f<T>(v[(int64_t)j * D + i]), acc[i]);
+                    for (int e = 0; e < 4; ++e) split_tf32(q[k][e], ah[e], al[e]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float* kp = kt + (n * 8 + g) * S::kLd + 8 * k + t;
+                        mma_3tf32(x[n], ah, al, kp[0], kp[4]);
+                    }
+                }
+                const int s0 = j * kFKT + wn * NT * 8 + 2 * t;      // token of x[0][0]
+                if ((j + 1) * kFKT > base_pos + tok0 + 1) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (s0 + 8 * n + (e & 1) > (e < 2 ? pos_a : pos_b)) x[n][e] = -SPLA_INF;
+                }
+                float ta = -SPLA_INF, tb = -SPLA_INF;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    ta = fmaxf(ta, fmaxf(x[n][0], x[n][1]));
+                    tb = fmaxf(tb, fmaxf(x[n][2], x[n][3]));
+                }
+                for (int d = 1; d < 4; d <<= 1) {
+                    ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, d));
+                    tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, d));
+                }
+                // log2 units from here on; sums are scaled by the running maximum
+                ta = fmaxf(m_a, ta * a.sl2);
+                tb = fmaxf(m_b, tb * a.sl2);
+                if (__any_sync(0xffffffffu, ta > m_a || tb > m_b)) {
+                    const float fa = m_a == -SPLA_INF ? 0.f : ex2(m_a - ta);
+                    const float fb = m_b == -SPLA_INF ? 0.f : ex2(m_b - tb);
+                    l_a *= fa;
+                    l_b *= fb;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[n][0] *= fa;
+                        o[n][1] *= fa;
+                        o[n][2] *= fb;
+                        o[n][3] *= fb;
+                    }
+                    m_a = ta;
+                    m_b = tb;
+                }
+                const float za = m_a == -SPLA_INF ? 0.f : m_a, zb = m_b == -SPLA_INF ? 0.f : m_b;
+                float sa = 0.f, sb = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    x[n][0] = ex2(fmaf(x[n][0], a.sl2, -za));
+                    x[n][1] = ex2(fmaf(x[n][1], a.sl2, -za));
+                    x[n][2] = ex2(fmaf(x[n][2], a.sl2, -zb));
+                    x[n][3] = ex2(fmaf(x[n][3], a.sl2, -zb));
+                    sa += x[n][0] + x[n][1];
+                    sb += x[n][2] + x[n][3];
+                }
+                l_a += sa;
+                l_b += sb;
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    // A's columns t and t + 4 are tokens 2t and 2t + 1
+                    uint32_t ah[4], al[4];
+                    split_tf32(x[k][0], ah[0], al[0]);
+                    split_tf32(x[k][2], ah[1], al[1]);
+                    split_tf32(x[k][1], ah[2], al[2]);
+                    split_tf32(x[k][3], ah[3], al[3]);
+                    const float* vp = vt + (k * 8 + 2 * t) * S::kLd + g;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+                        mma_3tf32(o[n], ah, al, vp[8 * n], vp[8 * n + S::kLd]);
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- the warps' sums meet where the tiles were
+        for (int d = 1; d < 4; d <<= 1) {
+            l_a += __shfl_xor_sync(0xffffffffu, l_a, d);
+            l_b += __shfl_xor_sync(0xffffffffu, l_b, d);
+        }
+        float* sum = f_smem;                        // [128][kLd]: row wn * kRows + row
+        float* sm = f_smem + 128 * S::kLd;
+        float* sl = sm + 128;
+        const int ra = wn * kRows + row_a, rb = wn * kRows + row_b;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+            *reinterpret_cast<float2*>(sum + ra * S::kLd + 8 * n + 2 * t) = make_float2(o[n][0], o[n][1]);
+            *reinterpret_cast<float2*>(sum + rb * S::kLd + 8 * n + 2 * t) = make_float2(o[n][2], o[n][3]);
+        }
+        if (t == 0) {
+            sm[ra] = m_a;
+            sm[rb] = m_b;
+            sl[ra] = l_a;
+            sl[rb] = l_b;
+        }
+        __syncthreads();
+        const bool whole = wk.j0 == 0 && wk.j1 == wk.T;
+        float* part = reinterpret_cast<float*>(a.ws + kCutBytes) +
+                      ((int64_t)blockIdx.x * 2 + (wk.j0 == 0 ? 1 : 0)) * part_floats(D);
+        for (int i = tid; i < kRows * (D / 4); i += kFThreads) {
+            const int row = i / (D / 4), x = (i - row * (D / 4)) * 4;
+            const int tok = tok0 + row / G;
+            if (tok >= wk.n) break;                 // rows ascend with i
+            float M = -SPLA_INF, l = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WN; ++w) M = fmaxf(M, sm[w * kRows + row]);
+#pragma unroll
+            for (int w = 0; w < WN; ++w) {
+                const float mw = sm[w * kRows + row], lw = sl[w * kRows + row];
+                // no tokens: no part; nothing but NaN logits: NaN
+                const float f = mw == -SPLA_INF ? (lw == lw ? 0.f : lw) : ex2(mw - M);
+                if (f == 0.f) continue;
+                const float4 v = *reinterpret_cast<const float4*>(sum + (w * kRows + row) * S::kLd + x);
+                l = fmaf(lw, f, l);
+                y.x = fmaf(v.x, f, y.x);
+                y.y = fmaf(v.y, f, y.y);
+                y.z = fmaf(v.z, f, y.z);
+                y.w = fmaf(v.w, f, y.w);
+            }
+            if (noted) {
+                const int pos = base_pos + tok;
+                y.x += note_term(first[0][x], first[1][x], first[2][x], pos);
+                y.y += note_term(first[0][x + 1], first[1][x + 1], first[2][x + 1], pos);
+                y.z += note_term(first[0][x + 2], first[1][x + 2], first[2][x + 2], pos);
+                y.w += note_term(first[0][x + 3], first[1][x + 3], first[2][x + 3], pos);
+            }
+            if (whole) {
+                const float inv = 1.f / l;
+                const int64_t orow = ((int64_t)wk.b * a.max_new + tok) * c.hq + wk.h * G + row % G;
+                *reinterpret_cast<float4*>((float*)a.out + orow * D + x) =
+                    make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                if (x == 0 && a.lse) a.lse[orow] = (M + log2f(l)) * 0.69314718055994531f;
+            } else {
+                *reinterpret_cast<float4*>(part + (int64_t)row * D + x) = y;
+                if (x == 0) {
+                    part[256 * D + row] = M;
+                    part[256 * D + 256 + row] = l;
+                }
+            }
+        }
+        wk.note_cut(cut, U, G, run);
+    }
+    if (tid == 0) reinterpret_cast<ChunkCut*>(a.ws)[blockIdx.x] = cut;
+}
+
+// ------------------------------------------------------------------ the join
+// One warp per row of a unit that was cut: log-sum-exp merge of its partials in run
+// order (the result does not depend on timing), lanes over the dimensions.
+constexpr int kJoinWarps = 8;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
+    constexpr int CPL = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = blockIdx.y, row = blockIdx.x * kJoinWarps + warp;
+    pdl_trigger();
+    pdl_wait();
+    const ChunkCut cut = reinterpret_cast<const ChunkCut*>(a.ws)[run];
+    if (row >= cut.rows || cut.parts == 0) return;
+    const float* base = reinterpret_cast<const float*>(a.ws + kCutBytes) +
+                        (int64_t)run * 2 * part_floats(D);
+    // partial p is run + p's, slot 1 for the first of them and slot 0 after it
+    auto part = [&](int p) { return base + ((int64_t)p * 2 + (p == 0 ? 1 : 0)) * part_floats(D); };
+    float M = -SPLA_INF;
+    for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, part(p)[256 * D + row]);
+    M = warp_max(M);
+    float l = 0.f, acc[CPL] = {};
+    for (int p0 = 0; p0 < cut.parts; p0 += 32) {
+        float w = 0.f;
+        if (p0 + lane < cut.parts) {
+            const float* q = part(p0 + lane);
+            const float m = q[256 * D + row];
+            const float lp = q[256 * D + 256 + row];
+            // no tokens: no part; nothing but NaN logits: NaN
+            w = m == -SPLA_INF ? (lp == lp ? 0.f : lp) : ex2(m - M);
+            l += w * lp;
+        }
+        const int cnt = min(32, cut.parts - p0);
+        constexpr int kBatch = 4;                   // partial rows in flight
+        for (int i = 0; i < cnt; i += kBatch) {
+            float x[kBatch][CPL];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (i + u < cnt) {
+                    const float* q = part(p0 + i + u) + (int64_t)row * D + lane * CPL;
+                    if constexpr (CPL == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(q);
+                    else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(q);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float f = __shfl_sync(0xffffffffu, w, (i + u) & 31);
+                if (i + u < cnt && f != 0.f)        // a partial without tokens has no part
+#pragma unroll
+                    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
+            }
         }
     }
-    T* o = (T*)a.out + row * D + lane * CPL;
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) o[i] = from_f<T>(acc[i] / l);
-    if (a.lse && lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+    l = warp_sum(l);
+    const int64_t orow = ((int64_t)cut.b * a.max_new + cut.t0 + row / c.group) * c.hq +
+                         cut.h * c.group + row % c.group;
+    const float inv = 1.f / l;
+    T* o = (T*)a.out + orow * D + lane * CPL;
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (CPL == 4)
+            *reinterpret_cast<float4*>(o) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv,
+                                                        acc[3] * inv);
+        else
+            *reinterpret_cast<float2*>(o) = make_float2(acc[0] * inv, acc[1] * inv);
+    } else if constexpr (CPL == 4) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                                                  pack_bf16(acc[2] * inv, acc[3] * inv));
+    } else {
+        *reinterpret_cast<uint32_t*>(o) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[orow] = (M + log2f(l)) * 0.69314718055994531f;
 }
 
-size_t chunk_tc_workspace_bytes(int d);
-
-size_t chunk_workspace_bytes(int d, int dtype) {
-    return dtype == SPLA_BF16 ? chunk_tc_workspace_bytes(d) : 256;
-}
-
-cudaError_t launch_chunk_simt(const CacheView& c, int dtype, const ChunkArgs& a, cudaStream_t s) {
-    const int64_t rows = (int64_t)c.batch * a.max_new * c.hq;
-    const dim3 grid((unsigned)((rows + kSimtWarps - 1) / kSimtWarps)), block(kSimtWarps * 32);
+// ------------------------------------------------------------------ host launchers
+cudaError_t launch_chunk_combine(const CacheView& c, int dtype, const ChunkArgs& a, int rows,
+                                 cudaStream_t s) {
+    const dim3 grid((rows + kJoinWarps - 1) / kJoinWarps, kMaxRuns), block(kJoinWarps * 32);
     using B16 = __nv_bfloat16;
     if (c.d == 128)
-        return dtype == SPLA_BF16 ? launch_pdl(chunk_simt_kernel<128, B16>, grid, block, 0, s, c, a)
-                                  : launch_pdl(chunk_simt_kernel<128, float>, grid, block, 0, s, c, a);
-    return dtype == SPLA_BF16 ? launch_pdl(chunk_simt_kernel<64, B16>, grid, block, 0, s, c, a)
-                              : launch_pdl(chunk_simt_kernel<64, float>, grid, block, 0, s, c, a);
+        return dtype == SPLA_BF16 ? launch_pdl(chunk_combine_kernel<128, B16>, grid, block, 0, s, c, a)
+                                  : launch_pdl(chunk_combine_kernel<128, float>, grid, block, 0, s, c, a);
+    return dtype == SPLA_BF16 ? launch_pdl(chunk_combine_kernel<64, B16>, grid, block, 0, s, c, a)
+                              : launch_pdl(chunk_combine_kernel<64, float>, grid, block, 0, s, c, a);
+}
+
+size_t chunk_workspace_bytes(int d) {
+    return kCutBytes + (size_t)kMaxRuns * 2 * part_floats(d) * sizeof(float);
+}
+
+template <int D, int WM>
+static cudaError_t launch_f32(const CacheView& c, const ChunkArgs& a, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(chunk_f32_kernel<D, WM>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)FShape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(chunk_f32_kernel<D, WM>, dim3(kMaxRuns), dim3(kFThreads), FShape<D>::kSmem, s, c, a);
+    if (e != cudaSuccess) return e;
+    const int rows = (int)std::min<int64_t>(16 * WM, (int64_t)a.max_new * c.group);
+    return launch_chunk_combine(c, SPLA_F32, a, rows, s);
+}
+
+// As few warps over the rows as hold the chunk, the others over the tokens.
+template <int D>
+static cudaError_t launch_f32_rows(const CacheView& c, const ChunkArgs& a, cudaStream_t s) {
+    const int64_t rows = (int64_t)a.max_new * c.group;
+    if (rows <= 16) return launch_f32<D, 1>(c, a, s);
+    if (rows <= 32) return launch_f32<D, 2>(c, a, s);
+    if (rows <= 64) return launch_f32<D, 4>(c, a, s);
+    return launch_f32<D, 8>(c, a, s);
+}
+
+cudaError_t launch_chunk_f32(const CacheView& c, const ChunkArgs& a, cudaStream_t s) {
+    return c.d == 128 ? launch_f32_rows<128>(c, a, s) : launch_f32_rows<64>(c, a, s);
 }
 
 }  // namespace spla

@@ -1,0 +1,207 @@
+// Chunk attention: what its kernels share. Exact causal attention of a chunk of new tokens
+// over the paged cache. With L_b tokens held by sequence b, the chunk's n_b among them,
+// query t of the chunk stands at position L_b - n_b + t and sees the tokens up to its own:
+//   o_t = sum_{s <= pos_t} p_ts v_s / sum p_ts,   p_ts = exp(scale q_t . k_s),
+//   lse_t = log sum_{s <= pos_t} p_ts
+// in one pass over the tokens with a running maximum (softmax attention as in the Baidu
+// article's section 1; the paged pools are the decode path's own).
+//
+// Rows. The G query heads that share a KV head and consecutive new tokens are the rows of
+// a tile (row = token * G + head), so a tile of K and V is read once for all of them. A
+// unit is one (sequence, KV head, block of U query tokens).
+//
+// Split. Every unit takes T = ceil(visible tokens / KT) steps over KT-token tiles of K and
+// V. All units' steps in a row, sum T = W of them, are cut into equal runs of
+// C = ceil(W / gridDim) steps, one per CTA (one CTA per SM), whatever the lengths: a
+// single long sequence, a ragged batch and many short prompts all fill the GPU evenly.
+// A unit that lies within one run is finished there; one that is cut leaves unnormalised
+// partial sums (O, l, and the maximum m they are scaled by, in log2 units), which
+// chunk_combine_kernel joins in run order, so results do not depend on timing.
+#pragma once
+
+#include "common.cuh"
+
+namespace spla {
+
+// What the split's run c left for the join, at its place in the workspace.
+struct ChunkCut {
+    int32_t parts;            // runs the unit that starts in run c and leaves it spans; 0: none
+    int32_t rows;             // its rows that hold queries
+    int32_t b, h, t0;         // sequence, KV head, first query token
+    int32_t pad[3];
+};
+
+constexpr int kMaxRuns = kNumSms;
+constexpr size_t kCutBytes = (sizeof(ChunkCut) * kMaxRuns + 255) / 256 * 256;
+// One partial: O [rows][d], then m [rows], l [rows]; run c has two (0: of the unit it
+// begins inside of, 1: of the unit it leaves unfinished).
+__host__ __device__ constexpr int64_t part_floats(int d) { return 256 * (int64_t)(d + 2); }
+
+// The chunk of sequence b; n = 0 where there is none or it is out of range.
+__device__ __forceinline__ void chunk_of(const CacheView& c, const ChunkArgs& a, int b,
+                                         int32_t* L, int32_t* n, bool flag) {
+    *L = c.lens[b];
+    *n = a.n_new[b];
+    int32_t bad = 0;
+    if (*n < 0 || *n > a.max_new) bad = SPLA_DEV_BAD_COUNT;
+    else if (*L < 0 || *L > (int64_t)c.mbp * c.bs) bad = SPLA_DEV_CAPACITY;
+    else if (*n > *L) bad = SPLA_DEV_BAD_COUNT;
+    if (bad) {
+        if (flag) set_status(a.status, bad);
+        *n = 0;
+        *L = 0;
+    }
+}
+
+// Steps of the units before query block qb of a sequence whose chunk starts at position
+// base: sum over i < qb of ceil((base + (i+1) U) / KT), one of U and KT a multiple of the
+// other.
+template <int KT>
+__device__ __forceinline__ int64_t steps_before(int64_t base, int64_t qb, int U) {
+    if (U >= KT) {
+        const int64_t k = U / KT;
+        return qb * ((base + KT - 1) / KT) + k * (qb * (qb + 1) / 2);
+    }
+    const int r = KT / U;                     // every r-th block adds a step to its class's
+    int64_t sum = 0;
+    for (int p = 0; p < r; ++p) {
+        const int64_t k = (qb - p + r - 1) / r;
+        sum += k * ((base + (int64_t)(p + 1) * U + KT - 1) / KT) + k * (k - 1) / 2;
+    }
+    return sum;
+}
+
+// A place in the row of all units' steps, and the walk over it that every role makes.
+template <int KT>
+struct Walk {
+    int b, h, qb;             // unit
+    int32_t L, n;             // its sequence's length and chunk
+    int j;                    // next step of the unit
+    int64_t left;             // steps left in this run
+    int j0, j1, T;            // the current segment [j0, j1) of the unit's T steps
+
+    __device__ __forceinline__ int units(int U) const { return (n + U - 1) / U; }
+    // Next segment of this run; false at its end.
+    __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int U) {
+        if (left <= 0) return false;
+        if (j < 0) {                                  // the last unit is done: go to the next
+            j = 0;
+            if (++qb >= units(U)) {
+                qb = 0;
+                if (++h >= c.hkv) {
+                    h = 0;
+                    n = 0;
+                    while (n == 0) {
+                        if (++b >= c.batch) return false;
+                        chunk_of(c, a, b, &L, &n, false);
+                    }
+                }
+            }
+        }
+        T = (int)((L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + KT - 1) / KT);
+        j0 = j;
+        j1 = (int)min((int64_t)T, j0 + left);
+        left -= j1 - j0;
+        j = j1 < T ? j1 : -1;
+        return true;
+    }
+    // Steps that query tile w of the unit takes part in end here.
+    __device__ __forceinline__ int tile_end(int w, int per_tile, int U) const {
+        const int64_t t0 = (int64_t)qb * U + (int64_t)w * per_tile;
+        if (t0 >= n) return 0;
+        const int64_t last = L - n + min(t0 + per_tile, (int64_t)n);
+        return min(j1, (int)((last + KT - 1) / KT));
+    }
+    // For the join: what the current segment leaves when its unit starts in it and goes on
+    // past this run of C steps.
+    __device__ __forceinline__ void note_cut(ChunkCut& cut, int U, int G, int64_t C) const {
+        if (j0 != 0 || j1 >= T) return;
+        cut.parts = 1 + (int)((T - j1 + C - 1) / C);
+        cut.rows = (int)min((int64_t)U, n - (int64_t)qb * U) * G;
+        cut.b = b;
+        cut.h = h;
+        cut.t0 = qb * U;
+    }
+};
+
+// This CTA's place, by all NT threads of it: contiguous sequences per thread, a scan over
+// the CTA. *start (start->left = 0 beforehand) and *run are for all after the call; scan
+// holds NT / 32 values. Two barriers.
+template <int KT, int NT>
+__device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a, int U,
+                                         int64_t* scan, Walk<KT>* start, int64_t* run) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (c.batch + NT - 1) / NT;
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= c.batch) break;
+        int32_t L, n;
+        chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
+        if (n) {
+            const int64_t q = (n + U - 1) / U;
+            mine += c.hkv * (steps_before<KT>(L - n, q - 1, U) + (L + KT - 1) / KT);
+        }
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t W = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) upto += scan[w];
+        W += scan[w];
+    }
+    const int64_t C = (W + gridDim.x - 1) / gridDim.x;
+    const int64_t f0 = (int64_t)blockIdx.x * C;
+    if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
+        int64_t at = f0 - (upto - mine);
+        Walk<KT> w;
+        for (int i = 0; i < per; ++i) {
+            w.b = tid * per + i;
+            chunk_of(c, a, w.b, &w.L, &w.n, false);
+            if (!w.n) continue;
+            const int64_t q = w.units(U), base = w.L - w.n;
+            const int64_t one = steps_before<KT>(base, q - 1, U) + (w.L + KT - 1) / KT;
+            if (at >= one * c.hkv) {
+                at -= one * c.hkv;
+                continue;
+            }
+            w.h = (int)(at / one);
+            at -= w.h * one;
+            int64_t lo = 0, hi = q - 1;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) / 2;
+                if (steps_before<KT>(base, mid, U) <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            w.qb = (int)lo;
+            w.j = (int)(at - steps_before<KT>(base, lo, U));
+            break;
+        }
+        w.left = min(C, W - f0);
+        *start = w;
+        *run = C;
+    }
+    __syncthreads();
+}
+
+// What infinities and NaN taken out of V (first[kind][dim]: the first token that holds
+// +inf, -inf, NaN there) add to a row at position pos.
+__device__ __forceinline__ float note_term(int32_t pinf, int32_t ninf, int32_t nan, int pos) {
+    float add = 0.f;
+    if (pinf <= pos) add += SPLA_INF;
+    if (ninf <= pos) add -= SPLA_INF;
+    if (nan <= pos) add = __int_as_float(0x7fffffff);
+    return add;
+}
+
+// Join launch for units of `rows` rows at most.
+cudaError_t launch_chunk_combine(const CacheView& c, int dtype, const ChunkArgs& a, int rows,
+                                 cudaStream_t s);
+
+}  // namespace spla

@@ -1,18 +1,7 @@
 // Chunk attention, bf16: the products on tcgen05 with logits, probabilities and outputs
-// in tensor memory. chunk_attn.cu states the mathematics.
-//
-// Rows. The G query heads that share a KV head and consecutive new tokens make the 128
-// rows of an MMA tile (row = token * G + head), so a tile of K and V is read once for
-// all of them. A unit is one (sequence, KV head, block of queries): two such tiles
-// (kTwo), or one where the whole chunk fits into it (n_new * G <= 128, decode included).
-//
-// Split. Every unit takes T = ceil(visible tokens / 128) steps over 128-token tiles of K
-// and V. All units' steps in a row, sum T = W of them, are cut into equal runs of
-// C = ceil(W / gridDim) steps, one per CTA (one CTA per SM), whatever the lengths: a
-// single long sequence, a ragged batch and many short prompts all fill the GPU evenly.
-// A unit that lies within one run is finished there; one that is cut leaves unnormalised
-// partial sums (O, l, and the maximum m they are scaled by), which
-// chunk_combine_kernel joins.
+// in tensor memory. chunk_attn.cuh states the mathematics and the split over the GPU; a
+// step here is 128 tokens, a unit two MMA tiles of 128 rows (kTwo), or one where the whole
+// chunk fits into it (n_new * G <= 128, decode included).
 //
 // Warps. 0-3 and 4-7: softmax of query tile 0 and 1 (one row per thread); 8: TMA (K and V
 // tiles page by page into a ring, query tiles; no multicast); 9: issues the MMAs, and
@@ -37,7 +26,7 @@
 // see that token.
 #include <algorithm>
 
-#include "common.cuh"
+#include "chunk_attn.cuh"
 
 namespace spla {
 
@@ -68,24 +57,6 @@ struct TcShape {
     static_assert(kStages >= 4, "the ring holds two steps");
     static_assert(kSmem <= kTcSmem, "shared memory");
 };
-
-// What the split's run c left for the join, at its place in the workspace.
-struct ChunkCut {
-    int32_t parts;            // runs the unit that starts in run c and leaves it spans; 0: none
-    int32_t rows;             // its rows that hold queries
-    int32_t b, h, t0;         // sequence, KV head, first query token
-    int32_t pad[3];
-};
-
-constexpr int kMaxRuns = kNumSms;
-constexpr size_t kCutBytes = (sizeof(ChunkCut) * kMaxRuns + 255) / 256 * 256;
-// One partial: O [rows][d], then m [rows], l [rows]; run c has two (0: of the unit it
-// begins inside of, 1: of the unit it leaves unfinished).
-__host__ __device__ constexpr int64_t part_floats(int d) { return 256 * (int64_t)(d + 2); }
-
-size_t chunk_tc_workspace_bytes(int d) {
-    return kCutBytes + (size_t)kMaxRuns * 2 * part_floats(d) * sizeof(float);
-}
 
 // ------------------------------------------------------------------ tcgen05 plumbing
 __device__ __forceinline__ void tcf_before() {
@@ -222,82 +193,13 @@ __device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* ba
         : "memory");
 }
 
-// ------------------------------------------------------------------ the split
-// The chunk of sequence b; n = 0 where there is none or it is out of range.
-__device__ __forceinline__ void tc_chunk_of(const CacheView& c, const ChunkArgs& a, int b,
-                                            int32_t* L, int32_t* n, bool flag) {
-    *L = c.lens[b];
-    *n = a.n_new[b];
-    int32_t bad = 0;
-    if (*n < 0 || *n > a.max_new) bad = SPLA_DEV_BAD_COUNT;
-    else if (*L < 0 || *L > (int64_t)c.mbp * c.bs) bad = SPLA_DEV_CAPACITY;
-    else if (*n > *L) bad = SPLA_DEV_BAD_COUNT;
-    if (bad) {
-        if (flag) set_status(a.status, bad);
-        *n = 0;
-        *L = 0;
-    }
-}
-
-// Steps of the units before query block qb of a sequence whose chunk starts at position
-// base: sum over i < qb of ceil((base + (i+1) U) / 128), U = 64, 128 or 256.
-__device__ __forceinline__ int64_t steps_before(int64_t base, int64_t qb, int U) {
-    if (U >= 128) {
-        const int64_t k = U / 128;
-        return qb * ((base + 127) / 128) + k * (qb * (qb + 1) / 2);
-    }
-    const int64_t ne = (qb + 1) / 2, no = qb / 2;
-    return ne * ((base + 64 + 127) / 128) + ne * (ne - 1) / 2 +
-           no * ((base + 128 + 127) / 128) + no * (no - 1) / 2;
-}
-
-// A place in the row of all units' steps, and the walk over it that every role makes.
-struct Walk {
-    int b, h, qb;             // unit
-    int32_t L, n;             // its sequence's length and chunk
-    int j;                    // next step of the unit
-    int64_t left;             // steps left in this run
-    int j0, j1, T;            // the current segment [j0, j1) of the unit's T steps
-
-    __device__ __forceinline__ int units(int U) const { return (n + U - 1) / U; }
-    // Next segment of this run; false at its end.
-    __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int U) {
-        if (left <= 0) return false;
-        if (j < 0) {                                  // the last unit is done: go to the next
-            j = 0;
-            if (++qb >= units(U)) {
-                qb = 0;
-                if (++h >= c.hkv) {
-                    h = 0;
-                    n = 0;
-                    while (n == 0) {
-                        if (++b >= c.batch) return false;
-                        tc_chunk_of(c, a, b, &L, &n, false);
-                    }
-                }
-            }
-        }
-        T = (L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + kTcTile - 1) / kTcTile;
-        j0 = j;
-        j1 = (int)min((int64_t)T, j0 + left);
-        left -= j1 - j0;
-        j = j1 < T ? j1 : -1;
-        return true;
-    }
-    // Position of the first query of tile w, and the steps that tile takes part in.
-    __device__ __forceinline__ int tile_end(int w, int per_tile, int U) const {
-        const int64_t t0 = (int64_t)qb * U + (int64_t)w * per_tile;
-        if (t0 >= n) return 0;
-        const int64_t last = L - n + min(t0 + per_tile, (int64_t)n);
-        return min(j1, (int)((last + kTcTile - 1) / kTcTile));
-    }
-};
+using TcWalk = Walk<kTcTile>;
 
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], fin;
     int64_t scan[kTcThreads / 32];
-    Walk start;
+    TcWalk start;
     int64_t run;                              // C
     uint32_t tmem;
     int32_t nf_seg;                           // segment whose infinities and NaN are noted
@@ -375,68 +277,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     pdl_wait();
     pdl_trigger();
 
-    // ---- this run's place: contiguous sequences per thread, a scan over the CTA
-    const int per = (c.batch + kTcThreads - 1) / kTcThreads;
-    int64_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b >= c.batch) break;
-        int32_t L, n;
-        tc_chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
-        if (n) {
-            const int64_t q = (n + U - 1) / U;
-            mine += c.hkv * (steps_before(L - n, q - 1, U) + (L + kTcTile - 1) / kTcTile);
-        }
-    }
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-    }
-    if (lane == 31) nt->scan[warp] = upto;
     tcf_before();
-    __syncthreads();
+    find_run<kTcTile, kTcThreads>(c, a, U, nt->scan, &nt->start, &nt->run);
     tcf_after();
-    int64_t W = 0;
-    for (int w = 0; w < kTcThreads / 32; ++w) {
-        if (w < warp) upto += nt->scan[w];
-        W += nt->scan[w];
-    }
-    const int64_t C = (W + gridDim.x - 1) / gridDim.x;
-    const int64_t f0 = (int64_t)blockIdx.x * C;
-    if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
-        int64_t at = f0 - (upto - mine);
-        Walk w;
-        for (int i = 0; i < per; ++i) {
-            w.b = tid * per + i;
-            tc_chunk_of(c, a, w.b, &w.L, &w.n, false);
-            if (!w.n) continue;
-            const int64_t q = w.units(U), base = w.L - w.n;
-            const int64_t one = steps_before(base, q - 1, U) + (w.L + kTcTile - 1) / kTcTile;
-            if (at >= one * c.hkv) {
-                at -= one * c.hkv;
-                continue;
-            }
-            w.h = (int)(at / one);
-            at -= w.h * one;
-            int64_t lo = 0, hi = q - 1;
-            while (lo < hi) {
-                const int64_t mid = (lo + hi + 1) / 2;
-                if (steps_before(base, mid, U) <= at) lo = mid;
-                else hi = mid - 1;
-            }
-            w.qb = (int)lo;
-            w.j = (int)(at - steps_before(base, lo, U));
-            break;
-        }
-        w.left = min(C, W - f0);
-        nt->start = w;
-        nt->run = C;
-    }
-    __syncthreads();
     const uint32_t tmem = nt->tmem;
-    Walk wk = nt->start;
+    TcWalk wk = nt->start;
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTcRegsLess));
@@ -786,13 +631,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         for (int k = 0; k < 32; ++k) o[k] = 0.f;
                     }
                     if (notes) {
-                        for (int k = 0; k < 32; ++k) {
-                            float add = 0.f;
-                            if (nt->first[0][i + k] <= pos) add += SPLA_INF;
-                            if (nt->first[1][i + k] <= pos) add -= SPLA_INF;
-                            if (nt->first[2][i + k] <= pos) add = __int_as_float(0x7fffffff);
-                            o[k] += add;
-                        }
+                        for (int k = 0; k < 32; ++k)
+                            o[k] += note_term(nt->first[0][i + k], nt->first[1][i + k],
+                                              nt->first[2][i + k], pos);
                     }
                     if (live && whole) {
                         uint4* d = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + orow * D + i);
@@ -818,13 +659,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     part[256 * D + 256 + row] = l;
                 }
             }
-            if (wk.j0 == 0 && wk.j1 < wk.T) {
-                cut.parts = 1 + (int)((wk.T - wk.j1 + nt->run - 1) / nt->run);
-                cut.rows = (int)min((int64_t)U, wk.n - (int64_t)wk.qb * U) * G;
-                cut.b = wk.b;
-                cut.h = wk.h;
-                cut.t0 = wk.qb * U;
-            }
+            wk.note_cut(cut, U, G, nt->run);
             __syncwarp();
             if (lane == 0) {
                 __threadfence_block();
@@ -839,73 +674,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     }
 }
 
-// ------------------------------------------------------------------ the join
-// One warp per row of a unit that was cut: log-sum-exp merge of its partials in run
-// order (the result does not depend on timing), lanes over the dimensions.
-constexpr int kJoinWarps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
-    constexpr int CPL = D / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int run = blockIdx.y, row = blockIdx.x * kJoinWarps + warp;
-    pdl_trigger();
-    pdl_wait();
-    const ChunkCut cut = reinterpret_cast<const ChunkCut*>(a.ws)[run];
-    if (row >= cut.rows || cut.parts == 0) return;
-    const float* base = reinterpret_cast<const float*>(a.ws + kCutBytes) +
-                        (int64_t)run * 2 * part_floats(D);
-    // partial p is run + p's, slot 1 for the first of them and slot 0 after it
-    auto part = [&](int p) { return base + ((int64_t)p * 2 + (p == 0 ? 1 : 0)) * part_floats(D); };
-    float M = -SPLA_INF;
-    for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, part(p)[256 * D + row]);
-    M = warp_max(M);
-    float l = 0.f, acc[CPL] = {};
-    for (int p0 = 0; p0 < cut.parts; p0 += 32) {
-        float w = 0.f;
-        if (p0 + lane < cut.parts) {
-            const float* q = part(p0 + lane);
-            const float m = q[256 * D + row];
-            const float lp = q[256 * D + 256 + row];
-            // no tokens: no part; nothing but NaN logits: NaN
-            w = m == -SPLA_INF ? (lp == lp ? 0.f : lp) : ex2(m - M);
-            l += w * lp;
-        }
-        const int cnt = min(32, cut.parts - p0);
-        constexpr int kBatch = 4;                   // partial rows in flight
-        for (int i = 0; i < cnt; i += kBatch) {
-            float x[kBatch][CPL];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (i + u < cnt) {
-                    const float* q = part(p0 + i + u) + (int64_t)row * D + lane * CPL;
-                    if constexpr (CPL == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(q);
-                    else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(q);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const float f = __shfl_sync(0xffffffffu, w, (i + u) & 31);
-                if (i + u < cnt && f != 0.f)        // a partial without tokens has no part
-#pragma unroll
-                    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
-            }
-        }
-    }
-    l = warp_sum(l);
-    const int64_t orow = ((int64_t)cut.b * a.max_new + cut.t0 + row / c.group) * c.hq +
-                         cut.h * c.group + row % c.group;
-    const float inv = 1.f / l;
-    __nv_bfloat16* o = (__nv_bfloat16*)a.out + orow * D + lane * CPL;
-    if constexpr (CPL == 4)
-        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                                  pack_bf16(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t*>(o) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (a.lse && lane == 0) a.lse[orow] = (M + log2f(l)) * 0.69314718055994531f;
-}
-
 // ------------------------------------------------------------------ host launcher
 template <int D, bool kTwo>
 static cudaError_t launch_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -918,8 +686,7 @@ static cudaError_t launch_tc(const CacheView& c, const CUtensorMap& tq, const CU
                    tv, c, a);
     if (e != cudaSuccess) return e;
     const int rows = (int)std::min<int64_t>(S::kRows, (int64_t)a.max_new * c.group);
-    return launch_pdl(chunk_combine_kernel<D>, dim3((rows + kJoinWarps - 1) / kJoinWarps, kMaxRuns),
-                      dim3(kJoinWarps * 32), 0, s, c, a);
+    return launch_chunk_combine(c, SPLA_BF16, a, rows, s);
 }
 
 // tq: [batch * max_new][Hq][d] with boxes of 64 dims x G heads x 128 / G tokens; tk, tv:

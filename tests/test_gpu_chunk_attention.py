@@ -105,6 +105,16 @@ def test_long_and_ragged(dtype, n_new):
     check(kv, q, [n_new] * 4, lens, out, lse)
 
 
+@pytest.mark.parametrize("dtype,L", [("bf16", 200003), ("f32", 60001)])
+@pytest.mark.parametrize("n_new", [1, 40])
+def test_one_long_sequence(dtype, L, n_new):
+    """Every thread block takes many steps in a row of one sequence."""
+    kv, q = build(30, [L], n_new, 4, 1, 64, 64, dtype)
+    out, lse = run(kv, q, [n_new])
+    check(kv, q, [n_new], [L], out, lse)
+    assert kv.status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_short_sequences(dtype):
     """More sequences than SMs, several whole ones a thread block."""
