@@ -23,6 +23,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int64_t kPlanRowsInline = 4096;       // four per thread of the one CTA
 constexpr int kRowsThreads = 256;
+constexpr int kRowsPerCta = 4 * kRowsThreads;
 
 struct BlockPoolView {
     int32_t* table;          // [batch][mbp]
@@ -79,9 +80,12 @@ plan_kernel(BlockPoolView p, const int32_t* lens, const int32_t* n_new, int32_t 
             int32_t* n_granted, int32_t* lens_after, int32_t* positions, int64_t* slots,
             int32_t* free_out, int rows_inline, int32_t* status) {
     __shared__ int64_t warp_tot[kPlanWarps];
-    __shared__ int32_t s_taken;
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid == 0) s_taken = 0;
+    __shared__ int32_t s_taken, s_base, s_end[kPlanThreads], s_dst[kPlanThreads];
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        s_taken = 0;
+        s_base = 0;
+    }
     pdl_wait();
     pdl_trigger();
     const int64_t cap = (int64_t)p.mbp * p.bs;
@@ -121,19 +125,31 @@ plan_kernel(BlockPoolView p, const int32_t* lens, const int32_t* n_new, int32_t 
             n_granted[b] = n;
             if (lens_after) lens_after[b] = len + n;
         }
-        // top of this sequence's share of the stack; entries go out downwards from it
-        const int32_t top = need ? (int32_t)(nfree - 1 - (upto - need)) : 0;
-        if (__reduce_max_sync(0xffffffffu, (unsigned)need) <= 2) {
-            for (int j = 0; j < need; ++j)
-                p.table[(int64_t)b * p.mbp + have + j] = p.free_list[top - j];
-        } else {
-            // long needs: the warp fills one sequence's row at a time, coalesced
-            for (int s = 0; s < 32; ++s) {
-                const int sn = __shfl_sync(0xffffffffu, need, s);
-                const int st = __shfl_sync(0xffffffffu, top, s);
-                const int sh = __shfl_sync(0xffffffffu, have, s);
-                int32_t* row = p.table + (int64_t)(b - lane + s) * p.mbp + sh;
-                for (int j = lane; j < sn; j += 32) row[j] = p.free_list[st - j];
+        // The round's new blocks in a row, entry i from the stack's place free - 1 - i: the
+        // threads take consecutive entries (coalesced) and find each one's sequence by its
+        // end in the scan. s_dst + i is the entry's place in its table row.
+        const int32_t before = s_base;
+        __syncthreads();                        // s_taken is final, s_base read
+        s_end[tid] = (int32_t)min(upto, (int64_t)s_taken);
+        s_dst[tid] = have - (int32_t)(upto - need);
+        if (tid == 0) s_base = s_taken;
+        __syncthreads();
+        for (int32_t i0 = before + tid; i0 < s_taken; i0 += 4 * kPlanThreads) {
+            int32_t blk[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int32_t i = i0 + u * kPlanThreads;
+                blk[u] = i < s_taken ? p.free_list[nfree - 1 - i] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int32_t i = i0 + u * kPlanThreads;
+                if (i >= s_taken) break;
+                int lo = 0;                     // the first sequence whose end is past i
+#pragma unroll
+                for (int w = kPlanThreads / 2; w; w >>= 1)
+                    if (s_end[lo + w - 1] <= i) lo += w;
+                p.table[(int64_t)(b0 + lo) * p.mbp + s_dst[lo] + i] = blk[u];
             }
         }
         __syncthreads();                        // warp_tot is free again; table rows visible
@@ -157,9 +173,13 @@ plan_rows_kernel(BlockPoolView p, const int32_t* lens, const int32_t* n_granted,
     for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
         const int32_t n = n_granted[b];
         const int32_t len = n > 0 ? lens[b] : 0;
-        for (int64_t t = blockIdx.x * kRowsThreads + threadIdx.x; t < max_new;
-             t += (int64_t)gridDim.x * kRowsThreads)
-            plan_row(p, (int64_t)b * max_new + t, b, (int)t, n, len, positions, slots, status);
+        const int64_t t0 = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < kRowsPerCta / kRowsThreads; ++u) {
+            const int64_t t = t0 + u * kRowsThreads;
+            if (t < max_new)
+                plan_row(p, (int64_t)b * max_new + t, b, (int)t, n, len, positions, slots, status);
+        }
     }
 }
 
@@ -265,7 +285,7 @@ cudaError_t launch_block_plan(const spla_block_pool* pool, const int32_t* lens,
                                max_new, n_granted, lens_after, positions, slots, free_out,
                                rows_inline, status);
     if (e != cudaSuccess || rows == 0 || rows_inline) return e;
-    const int tiles = (max_new + kRowsThreads - 1) / kRowsThreads;
+    const int tiles = (max_new + kRowsPerCta - 1) / kRowsPerCta;
     return launch_pdl(plan_rows_kernel, dim3(tiles, p.batch < 65535 ? p.batch : 65535),
                       dim3(kRowsThreads), 0, s, p, lens, n_granted, max_new, positions, slots,
                       status);

@@ -10,9 +10,9 @@
 // the shared memory, and these sizes are bound by the split's own instructions and by
 // shared-memory loads, not by the tensor pipe that tcgen05 would widen.
 //
-// A CTA of 8 warps: WM of them side by side over rows (16 each), 8 / WM over the tokens of
-// a 64-token step, chosen so that few rows (decode) still use every warp; their sums meet
-// in shared memory at the end of a segment. K and V tiles come through cp.async into a
+// A CTA of 8 or 16 warps: WM of them side by side over rows (16 each), the others over the
+// tokens of a 64-token step, chosen so that few rows (decode) still use every warp; their
+// sums meet in shared memory at the end of a segment. K and V tiles come through cp.async into a
 // two-stage ring, rows padded by 16 bytes (every fragment load is free of bank conflicts).
 // The probabilities' accumulator layout is the next product's A layout once the tokens of
 // a group of 8 are taken in the order 0 2 4 6 1 3 5 7, which the V loads follow.
@@ -27,15 +27,20 @@
 namespace spla {
 
 constexpr int kFKT = 64;                            // tokens of a step
-constexpr int kFThreads = 256;
 using FWalk = Walk<kFKT>;
 
-template <int D>
+template <int D, int WM>
 struct FShape {
+    // Warps: 16 where a thread's rows of O and Q fit 128 registers, 8 otherwise; a warp
+    // takes 8 tokens of a step at least.
+    static constexpr int kWarps = D == 64 && WM > 1 ? 16 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kWN = kWarps / WM;         // warps over the tokens
+    static constexpr int kNT = kFKT / 8 / kWN;      // token groups of 8 per warp and step
     static constexpr int kLd = D + 4;               // floats between tile rows
     static constexpr int kTile = kFKT * kLd;
-    static constexpr size_t kSmem = (size_t)4 * kTile * sizeof(float);
-    static_assert(128 * kLd + 256 <= 4 * kTile, "the warps' sums fit where the tiles were");
+    static constexpr int kSums = 16 * kWarps * (kLd + 2);   // the warps' sums, where the tiles were
+    static constexpr size_t kSmem = sizeof(float) * (kSums > 4 * kTile ? kSums : 4 * kTile);
 };
 
 __device__ __forceinline__ void cp_async16(float* dst, const float* src, bool live) {
@@ -48,28 +53,36 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 }
 // D += A (16x8, row) * B (8x8, col), tf32.
 __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_3tf32(float* c, const uint32_t* ah, const uint32_t* al,
-                                          float b0, float b1) {
-    uint32_t h0, l0, h1, l1;
-    split_tf32(b0, h0, l0);
-    split_tf32(b1, h1, l1);
-    mma_tf32(c, al, h0, h1);
-    mma_tf32(c, ah, l0, l1);
-    mma_tf32(c, ah, h0, h1);
+// N products with one A: the three parts of a product add to the same accumulator, so
+// they are issued N apart, small parts first.
+template <int N>
+__device__ __forceinline__ void mma_3tf32(float (*c)[4], const uint32_t* ah, const uint32_t* al,
+                                          const float* b0, const float* b1) {
+    uint32_t h0[N], l0[N], h1[N], l1[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        split_tf32(b0[n], h0[n], l0[n]);
+        split_tf32(b1[n], h1[n], l1[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma_tf32(c[n], al, h0[n], h1[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma_tf32(c[n], ah, l0[n], l1[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma_tf32(c[n], ah, h0[n], h1[n]);
 }
 
 template <int D, int WM>
-__global__ void __launch_bounds__(kFThreads, 1)
+__global__ void __launch_bounds__(FShape<D, WM>::kThreads, 1)
 chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
-    using S = FShape<D>;
-    constexpr int WN = 8 / WM, NT = 8 / WN;         // token groups of 8 per warp and step
-    constexpr int kRows = 16 * WM;
+    using S = FShape<D, WM>;
+    constexpr int WN = S::kWN, NT = S::kNT, kFThreads = S::kThreads;
+    constexpr int kRows = 16 * WM, kGrp = NT < 4 ? NT : 4;
     extern __shared__ __align__(16) float f_smem[];
     __shared__ int64_t scan[kFThreads / 32], run;
     __shared__ FWalk start;
@@ -94,6 +107,33 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
         const int tok_a = tok0 + row_a / G, tok_b = tok0 + row_b / G;
         const int pos_a = base_pos + tok_a, pos_b = base_pos + tok_b;
         const bool warp_live = tok0 + wm * 16 / G < wk.n;
+        float o[D / 8][4] = {};
+        float m_a = -SPLA_INF, m_b = -SPLA_INF, l_a = 0.f, l_b = 0.f;
+        __syncthreads();                            // the last segment's sums have been read
+        for (int i = tid; i < 3 * D; i += kFThreads) first[i / D][i % D] = 0x7fffffff;
+        if (tid == 0) noted = 0;
+
+        const int32_t* table = c.table + (int64_t)wk.b * c.mbp;
+        auto page_of = [&](int j) { return table[j * kFKT / c.bs]; };
+        auto load = [&](int j, int s, int32_t phys) {   // a step's tiles; slots past the end are zeros
+            const bool good = phys >= 0 && phys < c.num_phys;
+            if (!good && tid == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
+            const int64_t at = (((int64_t)(good ? phys : 0) * c.hkv + wk.h) * c.bs +
+                                ((j * kFKT) & (c.bs - 1))) * D;
+            const int held = good ? min(kFKT, wk.L - j * kFKT) : 0;
+#pragma unroll 4
+            for (int i = tid; i < kFKT * (D / 4); i += kFThreads) {
+                const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+                const int64_t src = at + (r < held ? (int64_t)r * D + x : 0);
+                cp_async16(ktile(s) + r * S::kLd + x, (const float*)c.k_pool + src, r < held);
+                cp_async16(vtile(s) + r * S::kLd + x, (const float*)c.v_pool + src, r < held);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int32_t page = page_of(wk.j0);
+        __syncthreads();
+        load(wk.j0, 0, page);
+        if (wk.j0 + 1 < wk.j1) page = page_of(wk.j0 + 1);
         float q[D / 8][4];
         {
             const float* qp = (const float*)a.q + ((int64_t)wk.b * a.max_new * c.hq + wk.h * G) * D;
@@ -107,35 +147,11 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 q[k][3] = tok_b < wk.n ? qb[8 * k + 4] : 0.f;
             }
         }
-        float o[D / 8][4] = {};
-        float m_a = -SPLA_INF, m_b = -SPLA_INF, l_a = 0.f, l_b = 0.f;
-        __syncthreads();                            // the last segment's sums have been read
-        for (int i = tid; i < 3 * D; i += kFThreads) first[i / D][i % D] = 0x7fffffff;
-        if (tid == 0) noted = 0;
-
-        const int32_t* table = c.table + (int64_t)wk.b * c.mbp;
-        auto load = [&](int j, int s) {             // a step's tiles; slots past the end are zeros
-            const int lb = j * kFKT / c.bs;
-            const int32_t phys = table[lb];
-            const bool good = phys >= 0 && phys < c.num_phys;
-            if (!good && tid == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
-            const int64_t at = (((int64_t)(good ? phys : 0) * c.hkv + wk.h) * c.bs +
-                                (j * kFKT - lb * c.bs)) * D;
-            const int held = good ? min(kFKT, wk.L - j * kFKT) : 0;
-            for (int i = tid; i < kFKT * (D / 4); i += kFThreads) {
-                const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
-                const int64_t src = at + (r < held ? (int64_t)r * D + x : 0);
-                cp_async16(ktile(s) + r * S::kLd + x, (const float*)c.k_pool + src, r < held);
-                cp_async16(vtile(s) + r * S::kLd + x, (const float*)c.v_pool + src, r < held);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        __syncthreads();
-        load(wk.j0, 0);
         for (int j = wk.j0; j < wk.j1; ++j) {
             const int s = (j - wk.j0) & 1;
             if (j + 1 < wk.j1) {
-                load(j + 1, s ^ 1);
+                load(j + 1, s ^ 1, page);
+                if (j + 2 < wk.j1) page = page_of(j + 2);   // a step ahead of its use
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             } else {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -168,9 +184,15 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) split_tf32(q[k][e], ah[e], al[e]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float* kp = kt + (n * 8 + g) * S::kLd + 8 * k + t;
-                        mma_3tf32(x[n], ah, al, kp[0], kp[4]);
+                    for (int n = 0; n < NT; n += kGrp) {
+                        float b0[kGrp], b1[kGrp];
+#pragma unroll
+                        for (int e = 0; e < kGrp; ++e) {
+                            const float* kp = kt + ((n + e) * 8 + g) * S::kLd + 8 * k + t;
+                            b0[e] = kp[0];
+                            b1[e] = kp[4];
+                        }
+                        mma_3tf32<kGrp>(x + n, ah, al, b0, b1);
                     }
                 }
                 const int s0 = j * kFKT + wn * NT * 8 + 2 * t;      // token of x[0][0]
@@ -232,8 +254,15 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                     split_tf32(x[k][3], ah[3], al[3]);
                     const float* vp = vt + (k * 8 + 2 * t) * S::kLd + g;
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        mma_3tf32(o[n], ah, al, vp[8 * n], vp[8 * n + S::kLd]);
+                    for (int n = 0; n < D / 8; n += 4) {
+                        float b0[4], b1[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            b0[e] = vp[8 * (n + e)];
+                            b1[e] = vp[8 * (n + e) + S::kLd];
+                        }
+                        mma_3tf32<4>(o + n, ah, al, b0, b1);
+                    }
                 }
             }
             __syncthreads();
@@ -244,9 +273,9 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
             l_a += __shfl_xor_sync(0xffffffffu, l_a, d);
             l_b += __shfl_xor_sync(0xffffffffu, l_b, d);
         }
-        float* sum = f_smem;                        // [128][kLd]: row wn * kRows + row
-        float* sm = f_smem + 128 * S::kLd;
-        float* sl = sm + 128;
+        float* sum = f_smem;                        // [16 kWarps][kLd]: row wn * kRows + row
+        float* sm = f_smem + 16 * S::kWarps * S::kLd;
+        float* sl = sm + 16 * S::kWarps;
         const int ra = wn * kRows + row_a, rb = wn * kRows + row_b;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
@@ -404,9 +433,10 @@ template <int D, int WM>
 static cudaError_t launch_f32(const CacheView& c, const ChunkArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(chunk_f32_kernel<D, WM>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)FShape<D>::kSmem);
+                                         (int)FShape<D, WM>::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(chunk_f32_kernel<D, WM>, dim3(kMaxRuns), dim3(kFThreads), FShape<D>::kSmem, s, c, a);
+    e = launch_pdl(chunk_f32_kernel<D, WM>, dim3(kMaxRuns), dim3(FShape<D, WM>::kThreads),
+                   FShape<D, WM>::kSmem, s, c, a);
     if (e != cudaSuccess) return e;
     const int rows = (int)std::min<int64_t>(16 * WM, (int64_t)a.max_new * c.group);
     return launch_chunk_combine(c, SPLA_F32, a, rows, s);

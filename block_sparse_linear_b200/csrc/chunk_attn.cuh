@@ -54,21 +54,27 @@ __device__ __forceinline__ void chunk_of(const CacheView& c, const ChunkArgs& a,
 }
 
 // Steps of the units before query block qb of a sequence whose chunk starts at position
-// base: sum over i < qb of ceil((base + (i+1) U) / KT), one of U and KT a multiple of the
-// other.
+// base: sum over i < qb of ceil((base + (i+1) U) / KT). U and KT are powers of two.
 template <int KT>
-__device__ __forceinline__ int64_t steps_before(int64_t base, int64_t qb, int U) {
+__device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U) {
     if (U >= KT) {
         const int64_t k = U / KT;
-        return qb * ((base + KT - 1) / KT) + k * (qb * (qb + 1) / 2);
+        return (int64_t)qb * ((base + KT - 1) / KT) + k * ((int64_t)qb * (qb + 1) / 2);
     }
-    const int r = KT / U;                     // every r-th block adds a step to its class's
+    // every r-th block of a class adds a step
+    const int lg = 31 - __clz(KT / U), r = 1 << lg;
     int64_t sum = 0;
     for (int p = 0; p < r; ++p) {
-        const int64_t k = (qb - p + r - 1) / r;
-        sum += k * ((base + (int64_t)(p + 1) * U + KT - 1) / KT) + k * (k - 1) / 2;
+        const int64_t k = (qb - p + r - 1) >> lg;
+        sum += k * ((base + (p + 1) * U + KT - 1) / KT) + k * (k - 1) / 2;
     }
     return sum;
+}
+
+// Steps of all of a sequence's units for one KV head.
+template <int KT>
+__device__ __forceinline__ int64_t steps_of(int32_t L, int32_t n, int U) {
+    return steps_before<KT>(L - n, (n + U - 1) / U - 1, U) + (L + KT - 1) / KT;
 }
 
 // A place in the row of all units' steps, and the walk over it that every role makes.
@@ -105,6 +111,10 @@ struct Walk {
         j = j1 < T ? j1 : -1;
         return true;
     }
+    // Whether the unit's queries reach past its first tile.
+    __device__ __forceinline__ bool pair(int per_tile, int U) const {
+        return (int64_t)qb * U + per_tile < n;
+    }
     // Steps that query tile w of the unit takes part in end here.
     __device__ __forceinline__ int tile_end(int w, int per_tile, int U) const {
         const int64_t t0 = (int64_t)qb * U + (int64_t)w * per_tile;
@@ -131,17 +141,14 @@ template <int KT, int NT>
 __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a, int U,
                                          int64_t* scan, Walk<KT>* start, int64_t* run) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int per = (c.batch + NT - 1) / NT;
+    const int per = ((unsigned)c.batch + NT - 1) / NT;
     int64_t mine = 0;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= c.batch) break;
         int32_t L, n;
         chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
-        if (n) {
-            const int64_t q = (n + U - 1) / U;
-            mine += c.hkv * (steps_before<KT>(L - n, q - 1, U) + (L + KT - 1) / KT);
-        }
+        if (n) mine += c.hkv * steps_of<KT>(L, n, U);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -156,7 +163,8 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         if (w < warp) upto += scan[w];
         W += scan[w];
     }
-    const int64_t C = (W + gridDim.x - 1) / gridDim.x;
+    const int64_t C = W <= INT32_MAX ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
+                                     : (W + gridDim.x - 1) / gridDim.x;
     const int64_t f0 = (int64_t)blockIdx.x * C;
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
         int64_t at = f0 - (upto - mine);
@@ -165,21 +173,20 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
             w.b = tid * per + i;
             chunk_of(c, a, w.b, &w.L, &w.n, false);
             if (!w.n) continue;
-            const int64_t q = w.units(U), base = w.L - w.n;
-            const int64_t one = steps_before<KT>(base, q - 1, U) + (w.L + KT - 1) / KT;
+            const int32_t base = w.L - w.n;
+            const int64_t one = steps_of<KT>(w.L, w.n, U);
             if (at >= one * c.hkv) {
                 at -= one * c.hkv;
                 continue;
             }
-            w.h = (int)(at / one);
-            at -= w.h * one;
-            int64_t lo = 0, hi = q - 1;
+            for (w.h = 0; at >= one; ++w.h) at -= one;
+            int32_t lo = 0, hi = w.units(U) - 1;
             while (lo < hi) {
-                const int64_t mid = (lo + hi + 1) / 2;
+                const int32_t mid = (lo + hi + 1) / 2;
                 if (steps_before<KT>(base, mid, U) <= at) lo = mid;
                 else hi = mid - 1;
             }
-            w.qb = (int)lo;
+            w.qb = lo;
             w.j = (int)(at - steps_before<KT>(base, lo, U));
             break;
         }

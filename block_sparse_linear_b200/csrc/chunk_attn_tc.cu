@@ -1,7 +1,7 @@
 // Chunk attention, bf16: the products on tcgen05 with logits, probabilities and outputs
 // in tensor memory. chunk_attn.cuh states the mathematics and the split over the GPU; a
-// step here is 128 tokens, a unit two MMA tiles of 128 rows (kTwo), or one where the whole
-// chunk fits into it (n_new * G <= 128, decode included).
+// step here is 128 tokens, a unit two MMA tiles of 128 rows (kTwo), or one where every
+// chunk of the call fits into it (max_new * G <= 128, decode included).
 //
 // Warps. 0-3 and 4-7: softmax of query tile 0 and 1 (one row per thread); 8: TMA (K and V
 // tiles page by page into a ring, query tiles; no multicast); 9: issues the MMAs, and
@@ -10,7 +10,8 @@
 //   P = exp2(sl2 S - m), rounded to bf16 over S's columns in tensor memory
 //   O += P V        M128 Nd K128, P from tensor memory, V as TMA wrote it (N-major)
 // The two query tiles alternate on the tensor pipe: one's products run while the other's
-// softmax does. With a single tile S is double-buffered instead.
+// softmax does. With a single tile, also in a unit of kTwo whose second tile is empty (a
+// decode in a batch of chunks), S is double-buffered instead.
 // The maximum a row's sums are scaled by follows the running maximum only when that has
 // grown by more than 2^8: until then the sums are merely larger, not less exact, and
 // the rescale of O (a pass over tensor memory) is skipped. l sums the probabilities
@@ -50,10 +51,13 @@ struct TcShape {
     static constexpr int kTileBytes = kTcTile * D * 2;       // a K, V or Q tile
     static constexpr int kBox = 8192;                        // 64 tokens x 64 dims
     static constexpr int kCtl = 2048;                        // barriers and notes
-    static constexpr int kFit = (kTcSmem - 1024 - kCtl - kQTiles * kTileBytes) / kTileBytes;
+    // Query tiles of two units where they fit beside the ring: short units then follow one
+    // another without a wait for their queries.
+    static constexpr int kQBufs = D == 64 ? 2 : 1;
+    static constexpr int kFit = (kTcSmem - 1024 - kCtl) / kTileBytes - kQTiles * kQBufs;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kRows = 128 * kQTiles;
-    static constexpr size_t kSmem = 1024 + kCtl + (size_t)(kQTiles + kStages) * kTileBytes;
+    static constexpr size_t kSmem = 1024 + kCtl + (size_t)(kQTiles * kQBufs + kStages) * kTileBytes;
     static_assert(kStages >= 4, "the ring holds two steps");
     static_assert(kSmem <= kTcSmem, "shared memory");
 };
@@ -197,7 +201,9 @@ using TcWalk = Walk<kTcTile>;
 
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], fin;
+    uint64_t q_full[2], q_empty[2];
+    // 0, 1: a pair of query tiles, tile w on buffer w; 2, 3: one tile on both buffers in turn
+    uint64_t s_full[4], p_full[4], o_done[4], fin;
     int64_t scan[kTcThreads / 32];
     TcWalk start;
     int64_t run;                              // C
@@ -241,7 +247,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     extern __shared__ unsigned char tc_smem_raw[];
     unsigned char* smem = tc_smem_raw + ((1024u - (smem_u32(tc_smem_raw) & 1023u)) & 1023u);
     unsigned char* qtile = smem;
-    unsigned char* ring = smem + S::kQTiles * S::kTileBytes;
+    unsigned char* ring = smem + S::kQTiles * S::kQBufs * S::kTileBytes;
     TcNotes* nt = reinterpret_cast<TcNotes*>(ring + S::kStages * S::kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = c.group;
@@ -253,9 +259,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(&nt->kv_full[s], 1);
             mbar_init(&nt->kv_empty[s], 1);
         }
-        mbar_init(&nt->q_full, 1);
-        mbar_init(&nt->q_empty, 1);
         for (int w = 0; w < 2; ++w) {
+            mbar_init(&nt->q_full[w], 1);
+            mbar_init(&nt->q_empty[w], 1);
+        }
+        for (int w = 0; w < 4; ++w) {
             mbar_init(&nt->s_full[w], 1);
             mbar_init(&nt->p_full[w], 4);
             mbar_init(&nt->o_done[w], 1);
@@ -292,16 +300,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         const int32_t none = (int32_t)((int64_t)c.num_phys * c.hkv * c.bs);   // reads as zeros
         const int upb = c.bs / 64;                      // 64-token rows of a page
         while (ok && wk.next(c, a, U)) {
-            if (seg > 0) ok = tc_wait(&nt->q_empty, (seg - 1) & 1, a.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&nt->q_full, S::kQTiles * S::kTileBytes);
-                for (int w = 0; w < S::kQTiles; ++w)
-                    for (int x = 0; x < S::kHalves; ++x)
-                        tma_q3(qtile + w * S::kTileBytes + x * 16384, &tq, &nt->q_full, 64 * x,
-                               wk.h * G, wk.b * a.max_new + wk.qb * U + w * per_tile);
-            }
             const int32_t* row = c.table + (int64_t)wk.b * c.mbp;
             const int nu = (wk.L + 63) / 64;            // 64-token rows the sequence holds
             int32_t ys = none;
@@ -337,19 +335,38 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     }
                 }
                 if (!ok) break;
+                if (j == wk.j0) {
+                    // the unit's queries, behind its first K and V: those need not wait for the
+                    // unit before to be done with its own
+                    const int qs = seg % S::kQBufs;
+                    if (seg >= S::kQBufs)
+                        ok = tc_wait(&nt->q_empty[qs], (seg / S::kQBufs - 1) & 1, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int tiles = wk.pair(per_tile, U) ? S::kQTiles : 1;
+                        mbar_arrive_expect_tx(&nt->q_full[qs], tiles * S::kTileBytes);
+                        for (int w = 0; w < tiles; ++w)
+                            for (int x = 0; x < S::kHalves; ++x)
+                                tma_q3(qtile + (qs * S::kQTiles + w) * S::kTileBytes + x * 16384, &tq,
+                                       &nt->q_full[qs], 64 * x, wk.h * G,
+                                       wk.b * a.max_new + wk.qb * U + w * per_tile);
+                    }
+                }
             }
             ++seg;
         }
         // the copies in flight have landed before the CTA may leave
         for (int i = max(0, it - S::kStages); i < it; ++i)
             mbar_wait_bounded(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1);
-        if (seg > 0) mbar_wait_bounded(&nt->q_full, (seg - 1) & 1);
+        for (int i = max(0, seg - S::kQBufs); i < seg; ++i)
+            mbar_wait_bounded(&nt->q_full[i % S::kQBufs], (i / S::kQBufs) & 1);
     } else if (warp == 9) {
         // ---------------------------------------------------------- MMA issuer
         constexpr uint32_t kIdS = tc_idesc(128, false), kIdO = tc_idesc(D, true);
         const uint32_t q0 = smem_u32(qtile), r0 = smem_u32(ring);
         int it = 0, seg = 0;
-        int ps[2] = {0, 0};                             // probabilities taken, per buffer
+        int ps[4] = {0, 0, 0, 0};                       // probabilities taken, per barrier
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool r = __all_sync(0xffffffffu, tc_wait(bar, parity, a.status));
@@ -364,17 +381,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         auto commit = [&](uint64_t* bar) {
             if (elect_one()) tc_commit(bar);
         };
-        auto do_s = [&](int w, int buf, int i) {        // S of query tile w by ring slot i
+        // S of the query tile at qs by ring slot i, into buffer bar & 1
+        auto do_s = [&](int qs, int bar, int i) {
             const uint32_t kd = uni(tc_desc_lo(r0 + (i % S::kStages) * S::kTileBytes, 16));
-            const uint32_t qd = uni(tc_desc_lo(q0 + w * S::kTileBytes, 16));
-            const uint32_t dst = uni(tmem + 128 * buf);
+            const uint32_t qd = uni(tc_desc_lo(q0 + qs * S::kTileBytes, 16));
+            const uint32_t dst = uni(tmem + 128 * (bar & 1));
+            uint64_t* done = &nt->s_full[bar];
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
                     mma_ss(dst, tc_desc(qd + off), tc_desc(kd + off), kIdS, kk != 0);
                 }
-                tc_commit(&nt->s_full[buf]);
+                tc_commit(done);
             }
         };
         auto do_o = [&](int w, int buf, int i, bool first) {
@@ -388,9 +407,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                            kk != 0 ? 1u : acc);
             }
         };
-        auto p_wait = [&](int buf) {
-            const bool r = wait(&nt->p_full[buf], ps[buf] & 1);
-            ++ps[buf];
+        auto p_wait = [&](int bar, int& count) {
+            const bool r = wait(&nt->p_full[bar], count & 1);
+            ++count;
             return r;
         };
         // V of step j is in; where some row does not see all of it, its rows past the
@@ -443,49 +462,53 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         };
         int buf = 0;                                    // S buffer of the next step (one tile)
         while (ok && wk.next(c, a, U)) {
-            if (!(ok = wait(&nt->q_full, seg & 1))) break;
+            const int qi = seg % S::kQBufs, qt = qi * S::kQTiles;
+            uint64_t* q_empty = &nt->q_empty[qi];
+            if (!(ok = wait(&nt->q_full[qi], (seg / S::kQBufs) & 1))) break;
             const int nj = wk.j1 - wk.j0;
-            if constexpr (kTwo) {
+            // slot it + 2 i is K of step i, it + 2 i + 1 its V
+            if (kTwo && wk.pair(per_tile, U)) {
                 const int e[2] = {wk.tile_end(0, per_tile, U), wk.tile_end(1, per_tile, U)};
-                // slot it + 2 i is K of step i, it + 2 i + 1 its V
                 if (!(ok = full(it))) break;
                 for (int w = 0; w < 2; ++w)
-                    if (wk.j0 < e[w]) do_s(w, w, it);
+                    if (wk.j0 < e[w]) do_s(qt + w, w, it);
                 commit(&nt->kv_empty[it % S::kStages]);
-                if (nj == 1) commit(&nt->q_empty);
+                if (nj == 1) commit(q_empty);
                 for (int i = 0; i < nj && ok; ++i) {
                     const int j = wk.j0 + i, iv = it + 2 * i + 1, ik = iv + 1;
                     if (!(ok = v_wait(j, iv))) break;
                     if (i + 1 < nj && !(ok = full(ik))) break;
+#pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         if (j >= e[w]) continue;
-                        if (!(ok = p_wait(w))) break;
+                        if (!(ok = p_wait(w, ps[w]))) break;
                         do_o(w, w, iv, i == 0);
-                        if (j + 1 < e[w]) do_s(w, w, ik);
+                        if (j + 1 < e[w]) do_s(qt + w, w, ik);
                         else commit(&nt->o_done[w]);
                     }
                     commit(&nt->kv_empty[iv % S::kStages]);
                     if (i + 1 < nj) commit(&nt->kv_empty[ik % S::kStages]);
-                    if (i + 2 == nj) commit(&nt->q_empty);
+                    if (i + 2 == nj) commit(q_empty);
                 }
             } else {
                 for (int i = 0; i < 2 && i < nj && ok; ++i) {
                     if (!(ok = full(it + 2 * i))) break;
-                    do_s(0, (buf + i) & 1, it + 2 * i);
+                    do_s(qt, 2 + ((buf + i) & 1), it + 2 * i);
                     commit(&nt->kv_empty[(it + 2 * i) % S::kStages]);
-                    if (i + 1 == nj) commit(&nt->q_empty);
+                    if (i + 1 == nj) commit(q_empty);
                 }
                 for (int i = 0; i < nj && ok; ++i, buf ^= 1) {
                     const int iv = it + 2 * i + 1, ik = iv + 3;
-                    if (!(ok = v_wait(wk.j0 + i, iv)) || !(ok = p_wait(buf))) break;
+                    if (!(ok = v_wait(wk.j0 + i, iv))) break;
+                    if (!(ok = buf ? p_wait(3, ps[3]) : p_wait(2, ps[2]))) break;
                     do_o(0, buf, iv, i == 0);
-                    commit(&nt->o_done[buf]);
+                    commit(&nt->o_done[2 + buf]);
                     commit(&nt->kv_empty[iv % S::kStages]);
                     if (i + 2 < nj) {
                         if (!(ok = full(ik))) break;
-                        do_s(0, buf, ik);
+                        do_s(qt, 2 + buf, ik);
                         commit(&nt->kv_empty[ik % S::kStages]);
-                        if (i + 3 == nj) commit(&nt->q_empty);
+                        if (i + 3 == nj) commit(q_empty);
                     }
                 }
             }
@@ -511,8 +534,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         const int r = tid & 127;                        // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;       // lane quarter, in the address
         const uint32_t tO = tmem + 256 + 128 * w + lanes;
-        int sc = 0;                                     // steps taken (this tile's S buffers)
-        int oc = 0;                                     // o_done phases passed before this segment
+        int pc = 0, oc = 0;                             // pairs: steps and segments of this tile
+        int sc = 0;                                     // one tile: steps
         int seg = 0;
         bool ok = true;
         ChunkCut cut = {};
@@ -521,14 +544,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const int tok = (int)t0 + r / G;            // query token of this row
             const bool live = tok < wk.n;
             const int pos = wk.L - wk.n + tok;
-            const int e = kTwo ? wk.tile_end(w, per_tile, U) : wk.j1;
+            const bool pair = kTwo && wk.pair(per_tile, U);
+            const int e = pair ? wk.tile_end(w, per_tile, U) : w == 0 ? wk.j1 : wk.j0;
             const int lo_pos = wk.L - wk.n + (int)t0;   // of the tile's first row
             const bool warp_live = (int)t0 + ((warp & 3) * 32) / G < wk.n;
             float m = -SPLA_INF, l = 0.f;
-            for (int j = wk.j0; j < e; ++j, ++sc) {
-                const int buf = kTwo ? w : sc & 1;
-                const uint32_t ph = kTwo ? sc & 1 : (sc >> 1) & 1;
-                ok = tc_wait(&nt->s_full[buf], ph, a.status);
+            for (int j = wk.j0; j < e; ++j) {
+                const int bar = pair ? w : 2 + (sc & 1), buf = bar & 1;
+                ok = tc_wait(&nt->s_full[bar], (pair ? pc : sc >> 1) & 1, a.status);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (warp_live) {
                     tcf_after();
@@ -555,9 +578,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2((m - top) * a.sl2) : 1.f;
                         l *= f;
-                        if (!kTwo && sc > 0 && j > wk.j0) {
+                        if (!pair && j > wk.j0) {
                             // the product of the step before may still be running
-                            ok = tc_wait(&nt->o_done[(sc - 1) & 1], ((sc - 1) >> 1) & 1, a.status);
+                            ok = tc_wait(&nt->o_done[2 + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1, a.status);
                             if (!(ok = __all_sync(0xffffffffu, ok))) break;
                             tcf_after();
                         }
@@ -595,7 +618,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     tcf_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&nt->p_full[buf]);
+                if (lane == 0) mbar_arrive(&nt->p_full[bar]);
+                if (pair) ++pc;
+                else ++sc;
             }
             if (!ok) break;
             // ---- this segment's sums
@@ -605,10 +630,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 // one tile: the products alternate between two barriers, since the one before
                 // the last may still be running here (never more: the last S was issued
                 // after the product two steps back)
-                ok = kTwo ? tc_wait(&nt->o_done[w], oc & 1, a.status)
-                          : tc_wait(&nt->o_done[(sc - 1) & 1], ((sc - 1) >> 1) & 1, a.status);
+                ok = pair ? tc_wait(&nt->o_done[w], oc & 1, a.status)
+                          : tc_wait(&nt->o_done[2 + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1, a.status);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                ++oc;
+                if (pair) ++oc;
                 tcf_after();
             }
             // a unit cut by this run's end starts a partial 1 unless it began before the run

@@ -15,7 +15,6 @@ One serving step of a model whose layers share a block table:
     cache.append(k_new, v_new, plan.n_granted)
     out = cache.decode(q)
 """
-import contextlib
 from collections import namedtuple
 
 import torch
@@ -24,28 +23,30 @@ from . import _lib
 
 BlockPlan = namedtuple("BlockPlan", "n_granted lens_after positions slots free_count")
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes `device` current for the launches of one call, where it is not already."""
-    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _elsewhere(device):
+    """Whether another device is current than the tensors' (launches go to the current one)."""
+    return torch.cuda.current_device() != device.index
 
 
 def _stream(device, stream):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)   # the handle without an object
 
 
 def _ptr(t):
-    return 0 if t is None else t.data_ptr()
+    return None if t is None else t.data_ptr()
+
+
+def _bad(t, name, dtype, shape, device):
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
+                     f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _need(t, name, dtype, shape, device):
     """A contiguous tensor of this type and shape on this device, or ValueError."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device \
-            or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _bad(t, name, dtype, shape, device)
 
 
 class SplaBlockPool:
@@ -91,18 +92,23 @@ class SplaBlockPool:
         rows) and free_count [1]. commit=False looks ahead: table rows and outputs are written,
         the blocks stay free."""
         dev, b = self.device, self.batch
-        _need(context_lens, "context_lens", torch.int32, (b,), dev)
-        _need(n_new, "n_new", torch.int32, (b,), dev)
-        with _on(dev):
-            i32 = dict(dtype=torch.int32, device=dev)
-            granted, after = torch.empty((2, b), **i32)
-            pos = torch.empty((b, max_new), **i32) if rows else None
-            slots = torch.empty((b, max_new), dtype=torch.int64, device=dev) if rows else None
-            left = self.free_count if commit else torch.empty((1,), **i32)
-            _lib.spla_block_plan(self.c, context_lens.data_ptr(), n_new.data_ptr(), max_new,
-                                 granted.data_ptr(), after.data_ptr(), _ptr(pos), _ptr(slots),
-                                 left.data_ptr(), self.dev_status.data_ptr(),
-                                 _stream(dev, stream))
+        shape = (b,)
+        _need(context_lens, "context_lens", torch.int32, shape, dev)
+        _need(n_new, "n_new", torch.int32, shape, dev)
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self.plan(context_lens, n_new, max_new, rows, commit, stream)
+        # one allocation for the counts
+        granted, after, left = n_new.new_empty(2 * b + 1).split((b, b, 1))
+        if commit:
+            left = self.free_count
+        pos = slots = None
+        if rows:
+            pos = n_new.new_empty((b, max_new))
+            slots = n_new.new_empty((b, max_new), dtype=torch.int64)
+        _lib.spla_block_plan(self.c, context_lens.data_ptr(), n_new.data_ptr(), max_new,
+                             granted.data_ptr(), after.data_ptr(), _ptr(pos), _ptr(slots),
+                             left.data_ptr(), self.dev_status.data_ptr(), _stream(dev, stream))
         return BlockPlan(granted, after, pos, slots, left)
 
     def release(self, keep_lens, context_lens, stream=None) -> None:
@@ -111,9 +117,11 @@ class SplaBlockPool:
         dev = self.device
         _need(keep_lens, "keep_lens", torch.int32, (self.batch,), dev)
         _need(context_lens, "context_lens", torch.int32, (self.batch,), dev)
-        with _on(dev):
-            _lib.spla_block_release(self.c, keep_lens.data_ptr(), context_lens.data_ptr(),
-                                    self.dev_status.data_ptr(), _stream(dev, stream))
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self.release(keep_lens, context_lens, stream)
+        _lib.spla_block_release(self.c, keep_lens.data_ptr(), context_lens.data_ptr(),
+                                self.dev_status.data_ptr(), _stream(dev, stream))
 
     def status(self) -> int:
         """Device-detected fault bits (synchronises)."""
@@ -122,33 +130,35 @@ class SplaBlockPool:
 
 def chunk_attention(owner, q, n_new, out=None, lse=None, lens=None, stream=None):
     """spla_chunk_attention over an owner's cache struct (SplaDecodeCache, SplaPagedKV)."""
-    cfg, dev = owner.cfg, owner.k_pool.device
+    p, dev = owner.params, owner.k_pool.device
     if q.dim() != 4:
         raise ValueError("q is [batch][max_new][Hq][d]")
-    b, T = owner.c.batch, int(q.shape[1])
-    _need(q, "q", cfg.torch_dtype, (b, T, cfg.num_q_heads, cfg.head_dim), dev)
+    b, T, hq = owner.c.batch, q.shape[1], p.num_q_heads
+    _need(q, "q", owner.k_pool.dtype, (b, T, hq, p.head_dim), dev)
     _need(n_new, "n_new", torch.int32, (b,), dev)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (b, T, cfg.num_q_heads), dev)
+        _need(lse, "lse", torch.float32, (b, T, hq), dev)
     c = owner.c
     if lens is not None:
         _need(lens, "lens", torch.int32, (b,), dev)
         c = _lib.spla_cache.from_buffer_copy(c)
         c.context_lens = lens.data_ptr()
-    with _on(dev):
-        if out is None:
-            out = torch.zeros_like(q)
-        else:
-            _need(out, "out", q.dtype, q.shape, dev)
-        # one size whatever the chunk, so that a captured call and later eager ones never
-        # see it replaced
-        if owner._chunk_ws is None:
-            need = _lib.spla_chunk_attention_workspace_size(owner.params, b, T)
-            owner._chunk_ws = torch.empty((need + 255) // 256 * 256, dtype=torch.uint8, device=dev)
-        ws = owner._chunk_ws
-        _lib.spla_chunk_attention(owner.params, c, q.data_ptr(), n_new.data_ptr(), T,
-                                  out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                                  owner.dev_status.data_ptr(), _stream(dev, stream))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return chunk_attention(owner, q, n_new, out, lse, lens, stream)
+    if out is None:
+        out = torch.zeros_like(q)
+    else:
+        _need(out, "out", q.dtype, q.shape, dev)
+    # one size whatever the chunk, so that a captured call and later eager ones never see it
+    # replaced
+    if owner._chunk_ws is None:
+        need = _lib.spla_chunk_attention_workspace_size(p, b, T)
+        owner._chunk_ws = torch.empty((need + 255) // 256 * 256, dtype=torch.uint8, device=dev)
+    ws = owner._chunk_ws
+    _lib.spla_chunk_attention(p, c, q.data_ptr(), n_new.data_ptr(), T, out.data_ptr(),
+                              _ptr(lse), ws.data_ptr(), ws.numel(), owner.dev_status.data_ptr(),
+                              _stream(dev, stream))
     return out
 
 
@@ -194,18 +204,19 @@ class SplaPagedKV:
 
 def _flat(t, name, dtype, n, device):
     """A contiguous tensor of n elements, whatever its shape, or ValueError."""
-    if t.numel() != n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-    _need(t, name, dtype, t.shape, device)
+    if t.numel() != n or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {n} elements on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(t, name, heads, d, dtype, device):
     """Row stride of a [rows][heads][d] view whose heads lie side by side."""
-    if t.dim() != 3 or t.shape[1:] != (heads, d) or t.dtype != dtype or t.device != device \
-            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not dtype \
+            or t.device != device or stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{name}: expected a {dtype} [rows][{heads}][{d}] tensor on {device} "
                          "whose heads lie side by side")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+    return stride[0] if shape[0] > 1 else max(stride[0], heads * d)
 
 
 def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=None, eps=1e-6,
@@ -221,7 +232,7 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
     slots; tensors made here hold zeros in skipped rows."""
     hq, hkv, d, dt, dev = (cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.torch_dtype,
                            q.device)
-    rows = int(q.shape[0])
+    rows = q.shape[0]
     qs, ks = _rows(q, "q", hq, d, dt, dev), _rows(k, "k", hkv, d, dt, dev)
     vs = _rows(v, "v", hkv, d, dt, dev) if v is not None else 0
     if k.shape[0] != rows or (v is not None and v.shape[0] != rows):
@@ -229,38 +240,41 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
     _flat(positions, "positions", torch.int32, rows, dev)
     rot = 0
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev)
         rot = 2 * inv_freq.numel()
-    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
-        if g is not None:
-            _need(g, name, torch.float32, (d,), dev)
-    with _on(dev):
-        if q_out is None:
-            q_out = torch.zeros((rows, hq, d), dtype=dt, device=dev)
-        else:
-            _flat(q_out, "q_out", dt, rows * hq * d, dev)
+        _flat(inv_freq, "inv_freq", torch.float64, rot // 2, dev)
+    if q_gamma is not None:
+        _need(q_gamma, "q_gamma", torch.float32, (d,), dev)
+    if k_gamma is not None:
+        _need(k_gamma, "k_gamma", torch.float32, (d,), dev)
+    if (slots is None) != (kv is None) or (kv is not None and (k_out is not None or v_out is not None)):
+        raise ValueError("kv and slots go together, and without k_out and v_out")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return qk_norm_rope(cfg, q, k, v, positions, inv_freq, q_gamma, k_gamma, eps, interleaved,
+                                q_out, k_out, v_out, kv, slots, dev_status, stream)
+    if q_out is None:
+        q_out = torch.zeros((rows, hq, d), dtype=dt, device=dev)
+    else:
+        _flat(q_out, "q_out", dt, rows * hq * d, dev)
+    if kv is not None:
+        _flat(slots, "slots", torch.int64, rows, dev)
+        kp, vp, phys = kv.k_pool, kv.v_pool, kv.num_phys_blocks
+        _need(kp, "kv.k_pool", dt, (phys, hkv, cfg.block_size, d), dev)
+        if dev_status is None:
+            dev_status = kv.dev_status
+    else:
         phys = 0
-        if slots is not None:
-            if kv is None or k_out is not None or v_out is not None:
-                raise ValueError("slots go with kv, and without k_out and v_out")
-            _flat(slots, "slots", torch.int64, rows, dev)
-            pool = (kv.num_phys_blocks, hkv, cfg.block_size, d)
-            _need(kv.k_pool, "kv.k_pool", dt, pool, dev)
-            kp, vp, phys = kv.k_pool, kv.v_pool, kv.num_phys_blocks
+        if k_out is None:
+            k_out = torch.zeros((rows, hkv, d), dtype=dt, device=dev)
         else:
-            if kv is not None:
-                raise ValueError("kv goes with slots")
-            if k_out is None:
-                k_out = torch.zeros((rows, hkv, d), dtype=dt, device=dev)
-            if v_out is None and v is not None:
-                v_out = torch.zeros((rows, hkv, d), dtype=dt, device=dev)
             _flat(k_out, "k_out", dt, rows * hkv * d, dev)
-            if v_out is not None:
-                _flat(v_out, "v_out", dt, rows * hkv * d, dev)
-            kp, vp = k_out, v_out
-        status = dev_status if dev_status is not None else getattr(kv, "dev_status", None)
-        _lib.spla_qk_norm_rope(cfg.params(), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, rows,
-                               positions.data_ptr(), _ptr(inv_freq), rot, int(interleaved),
-                               _ptr(q_gamma), _ptr(k_gamma), eps, q_out.data_ptr(), kp.data_ptr(),
-                               _ptr(vp), _ptr(slots), phys, _ptr(status), _stream(dev, stream))
-    return q_out if slots is not None else (q_out, k_out, v_out)
+        if v_out is not None:
+            _flat(v_out, "v_out", dt, rows * hkv * d, dev)
+        elif v is not None:
+            v_out = torch.zeros((rows, hkv, d), dtype=dt, device=dev)
+        kp, vp = k_out, v_out
+    _lib.spla_qk_norm_rope(cfg.params(), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, rows,
+                           positions.data_ptr(), _ptr(inv_freq), rot, interleaved, _ptr(q_gamma),
+                           _ptr(k_gamma), eps, q_out.data_ptr(), kp.data_ptr(), _ptr(vp),
+                           _ptr(slots), phys, _ptr(dev_status), _stream(dev, stream))
+    return q_out if kv is not None else (q_out, k_out, v_out)

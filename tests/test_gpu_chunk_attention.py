@@ -116,6 +116,19 @@ def test_one_long_sequence(dtype, L, n_new):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,block", [(64, 64), (128, 128)])
+def test_decodes_and_chunks_in_one_batch(dtype, d, block):
+    """Single tokens, drafts and chunks of several tiles side by side, so that units of one
+    tile and of two follow one another within a thread block."""
+    lens = [5000, 9000, 300, 4000, 1, 777, 2500, 90]
+    n_new = [1, 200, 40, 33, 1, 129, 0, 65]
+    kv, q = build(31, lens, 200, 8, 2, d, block, dtype)
+    out, lse = run(kv, q, n_new)
+    check(kv, q, n_new, lens, out, lse)
+    assert kv.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_short_sequences(dtype):
     """More sequences than SMs, several whole ones a thread block."""
     lens = [1 + (37 * i) % 200 for i in range(180)]
