@@ -3,15 +3,17 @@
 // step here is 128 tokens, a unit two MMA tiles of 128 rows (kTwo), or one where every
 // chunk of the call fits into it (max_new * G <= 128, decode included).
 //
-// Warps. 0-3 and 4-7: softmax of query tile 0 and 1 (one row per thread); 8: TMA (K and V
-// tiles page by page into a ring, query tiles; no multicast); 9: issues the MMAs, and
-// looks over the V tiles that some row does not see whole.
+// Warps. 0-3 and 4-7: softmax of two streams (one row per thread); 8: TMA (K and V tiles
+// page by page into a ring, query tiles; no multicast); 9: issues the MMAs, and looks over
+// the V tiles that some row does not see whole.
 //   S = Q K^T       M128 N128 Kd, both operands in shared memory as TMA wrote them
 //   P = exp2(sl2 S - m), rounded to bf16 over S's columns in tensor memory
 //   O += P V        M128 Nd K128, P from tensor memory, V as TMA wrote it (N-major)
-// The two query tiles alternate on the tensor pipe: one's products run while the other's
-// softmax does. With a single tile, also in a unit of kTwo whose second tile is empty (a
-// decode in a batch of chunks), S is double-buffered instead.
+// The streams alternate on the tensor pipe: one's products run while the other's softmax
+// does. In a unit of two query tiles a stream is a tile; in a unit of one, it is every other
+// step of that tile, with an O of its own, and stream 0's epilogue adds the two (both stand
+// in the same lanes). A step's softmax takes longer than its K and V take to come from
+// memory: one stream alone bounds a decode by its exponentials (16 a clock and SM).
 // The maximum a row's sums are scaled by follows the running maximum only when that has
 // grown by more than 2^8: until then the sums are merely larger, not less exact, and
 // the rescale of O (a pass over tensor memory) is skipped. l sums the probabilities
@@ -50,14 +52,14 @@ struct TcShape {
     static constexpr int kHalves = D / 64;                   // 64-dimension boxes across a row
     static constexpr int kTileBytes = kTcTile * D * 2;       // a K, V or Q tile
     static constexpr int kBox = 8192;                        // 64 tokens x 64 dims
-    static constexpr int kCtl = 2048;                        // barriers and notes
+    static constexpr int kCtl = 3072;                        // barriers and notes
     // Query tiles of two units where they fit beside the ring: short units then follow one
     // another without a wait for their queries.
     static constexpr int kQBufs = D == 64 ? 2 : 1;
-    static constexpr int kFit = (kTcSmem - 1024 - kCtl) / kTileBytes - kQTiles * kQBufs;
+    static constexpr int kFit = (kTcSmem - kCtl) / kTileBytes - kQTiles * kQBufs;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kRows = 128 * kQTiles;
-    static constexpr size_t kSmem = 1024 + kCtl + (size_t)(kQTiles * kQBufs + kStages) * kTileBytes;
+    static constexpr size_t kSmem = kCtl + (size_t)(kQTiles * kQBufs + kStages) * kTileBytes;
     static_assert(kStages >= 4, "the ring holds two steps");
     static_assert(kSmem <= kTcSmem, "shared memory");
 };
@@ -202,8 +204,8 @@ using TcWalk = Walk<kTcTile>;
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
     uint64_t q_full[2], q_empty[2];
-    // 0, 1: a pair of query tiles, tile w on buffer w; 2, 3: one tile on both buffers in turn
-    uint64_t s_full[4], p_full[4], o_done[4], fin;
+    uint64_t s_full[2], p_full[2], o_done[2]; // by stream
+    uint64_t m_full, m_empty, fin;            // stream 1's sums for stream 0's epilogue
     int64_t scan[kTcThreads / 32];
     TcWalk start;
     int64_t run;                              // C
@@ -211,8 +213,9 @@ struct TcNotes {                              // control block in shared memory
     int32_t nf_seg;                           // segment whose infinities and NaN are noted
     int32_t epi;                              // warps past an epilogue, over all segments
     int32_t first[3][128];                    // first token with +inf, -inf, NaN, per dimension
+    float m1[128], l1[128];
 };
-static_assert(sizeof(TcNotes) <= 2048, "control block");
+static_assert(sizeof(TcNotes) <= 3072, "control block");
 
 // Bounded waits. A role may sit out another's whole run (thousands of steps), so the
 // bound is a time, looked at every 1024 polls, with a count over it.
@@ -244,10 +247,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const CacheView c, const ChunkArgs a) {
     using S = TcShape<D, kTwo>;
-    extern __shared__ unsigned char tc_smem_raw[];
-    unsigned char* smem = tc_smem_raw + ((1024u - (smem_u32(tc_smem_raw) & 1023u)) & 1023u);
-    unsigned char* qtile = smem;
-    unsigned char* ring = smem + S::kQTiles * S::kQBufs * S::kTileBytes;
+    extern __shared__ __align__(1024) unsigned char tc_smem[];      // swizzle atoms are 1024 bytes
+    unsigned char* qtile = tc_smem;
+    unsigned char* ring = tc_smem + S::kQTiles * S::kQBufs * S::kTileBytes;
     TcNotes* nt = reinterpret_cast<TcNotes*>(ring + S::kStages * S::kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = c.group;
@@ -263,7 +265,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(&nt->q_full[w], 1);
             mbar_init(&nt->q_empty[w], 1);
         }
-        for (int w = 0; w < 4; ++w) {
+        mbar_init(&nt->m_full, 4);
+        mbar_init(&nt->m_empty, 4);
+        for (int w = 0; w < 2; ++w) {
             mbar_init(&nt->s_full[w], 1);
             mbar_init(&nt->p_full[w], 4);
             mbar_init(&nt->o_done[w], 1);
@@ -366,7 +370,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         constexpr uint32_t kIdS = tc_idesc(128, false), kIdO = tc_idesc(D, true);
         const uint32_t q0 = smem_u32(qtile), r0 = smem_u32(ring);
         int it = 0, seg = 0;
-        int ps[4] = {0, 0, 0, 0};                       // probabilities taken, per barrier
+        int ps[2] = {0, 0};                             // probabilities taken, per stream
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool r = __all_sync(0xffffffffu, tc_wait(bar, parity, a.status));
@@ -381,12 +385,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         auto commit = [&](uint64_t* bar) {
             if (elect_one()) tc_commit(bar);
         };
-        // S of the query tile at qs by ring slot i, into buffer bar & 1
-        auto do_s = [&](int qs, int bar, int i) {
+        // S of the query tile at qs by ring slot i, for stream w
+        auto do_s = [&](int qs, int w, int i) {
             const uint32_t kd = uni(tc_desc_lo(r0 + (i % S::kStages) * S::kTileBytes, 16));
             const uint32_t qd = uni(tc_desc_lo(q0 + qs * S::kTileBytes, 16));
-            const uint32_t dst = uni(tmem + 128 * (bar & 1));
-            uint64_t* done = &nt->s_full[bar];
+            const uint32_t dst = uni(tmem + 128 * w);
+            uint64_t* done = &nt->s_full[w];
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -396,9 +400,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 tc_commit(done);
             }
         };
-        auto do_o = [&](int w, int buf, int i, bool first) {
+        auto do_o = [&](int w, int i, bool first) {
             const uint32_t vd = uni(tc_desc_lo(r0 + (i % S::kStages) * S::kTileBytes, 16384));
-            const uint32_t dst = uni(tmem + 256 + 128 * w), src = uni(tmem + 128 * buf);
+            const uint32_t dst = uni(tmem + 256 + 128 * w), src = uni(tmem + 128 * w);
             const uint32_t acc = uni(first ? 0u : 1u);
             if (elect_one()) {
 #pragma unroll
@@ -407,8 +411,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                            kk != 0 ? 1u : acc);
             }
         };
-        auto p_wait = [&](int bar, int& count) {
-            const bool r = wait(&nt->p_full[bar], count & 1);
+        auto p_wait = [&](int w, int& count) {
+            const bool r = wait(&nt->p_full[w], count & 1);
             ++count;
             return r;
         };
@@ -437,7 +441,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     // the rows of the segments before have read their notes
                     const volatile int32_t* epi = &nt->epi;
                     const unsigned long long t1 = global_ns();
-                    while (*epi < 4 * S::kQTiles * seg && global_ns() - t1 < kTcWaitNs) {}
+                    while (*epi < 8 * seg && global_ns() - t1 < kTcWaitNs) {}
                     __syncwarp();
                     for (int x = lane; x < 3 * 128; x += 32) nt->first[x / 128][x % 128] = 0x7fffffff;
                     if (lane == 0) nt->nf_seg = seg;
@@ -460,7 +464,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             __syncwarp();
             return true;
         };
-        int buf = 0;                                    // S buffer of the next step (one tile)
         while (ok && wk.next(c, a, U)) {
             const int qi = seg % S::kQBufs, qt = qi * S::kQTiles;
             uint64_t* q_empty = &nt->q_empty[qi];
@@ -482,7 +485,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     for (int w = 0; w < 2; ++w) {
                         if (j >= e[w]) continue;
                         if (!(ok = p_wait(w, ps[w]))) break;
-                        do_o(w, w, iv, i == 0);
+                        do_o(w, iv, i == 0);
                         if (j + 1 < e[w]) do_s(qt + w, w, ik);
                         else commit(&nt->o_done[w]);
                     }
@@ -493,20 +496,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             } else {
                 for (int i = 0; i < 2 && i < nj && ok; ++i) {
                     if (!(ok = full(it + 2 * i))) break;
-                    do_s(qt, 2 + ((buf + i) & 1), it + 2 * i);
+                    do_s(qt, i, it + 2 * i);
                     commit(&nt->kv_empty[(it + 2 * i) % S::kStages]);
                     if (i + 1 == nj) commit(q_empty);
                 }
-                for (int i = 0; i < nj && ok; ++i, buf ^= 1) {
-                    const int iv = it + 2 * i + 1, ik = iv + 3;
+                for (int i = 0; i < nj && ok; ++i) {
+                    const int w = i & 1, iv = it + 2 * i + 1, ik = iv + 3;
                     if (!(ok = v_wait(wk.j0 + i, iv))) break;
-                    if (!(ok = buf ? p_wait(3, ps[3]) : p_wait(2, ps[2]))) break;
-                    do_o(0, buf, iv, i == 0);
-                    commit(&nt->o_done[2 + buf]);
+                    if (!(ok = w ? p_wait(1, ps[1]) : p_wait(0, ps[0]))) break;
+                    do_o(w, iv, i < 2);
+                    if (i + 2 >= nj) commit(&nt->o_done[w]);
                     commit(&nt->kv_empty[iv % S::kStages]);
                     if (i + 2 < nj) {
                         if (!(ok = full(ik))) break;
-                        do_s(qt, 2 + buf, ik);
+                        do_s(qt, w, ik);
                         commit(&nt->kv_empty[ik % S::kStages]);
                         if (i + 3 == nj) commit(q_empty);
                     }
@@ -528,34 +531,34 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     }
     } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kTcRegsMore));
-    if (kTwo || warp < 4) {
+    {
         // ---------------------------------------------------------- softmax and epilogue
-        const int w = warp >> 2;                        // query tile
+        const int w = warp >> 2;                        // stream
         const int r = tid & 127;                        // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;       // lane quarter, in the address
         const uint32_t tO = tmem + 256 + 128 * w + lanes;
-        int pc = 0, oc = 0;                             // pairs: steps and segments of this tile
-        int sc = 0;                                     // one tile: steps
+        int sc = 0, oc = 0, mc = 0;                     // steps, segments with steps, joins
         int seg = 0;
         bool ok = true;
         ChunkCut cut = {};
         while (ok && wk.next(c, a, U)) {
-            const int64_t t0 = (int64_t)wk.qb * U + w * per_tile;
-            const int tok = (int)t0 + r / G;            // query token of this row
+            // a pair: stream w is query tile w, every step; one tile: every other step of it
+            const bool pair = kTwo && wk.pair(per_tile, U);
+            const int t0 = wk.qb * U + (pair ? w * per_tile : 0);
+            const int tok = t0 + r / G;                 // query token of this row
             const bool live = tok < wk.n;
             const int pos = wk.L - wk.n + tok;
-            const bool pair = kTwo && wk.pair(per_tile, U);
-            const int e = pair ? wk.tile_end(w, per_tile, U) : w == 0 ? wk.j1 : wk.j0;
-            const int lo_pos = wk.L - wk.n + (int)t0;   // of the tile's first row
-            const bool warp_live = (int)t0 + ((warp & 3) * 32) / G < wk.n;
+            const int lo_pos = wk.L - wk.n + t0;        // of the tile's first row
+            const bool warp_live = t0 + ((warp & 3) * 32) / G < wk.n;
+            const int first_j = wk.j0 + (pair ? 0 : w), by = pair ? 1 : 2;
+            const int e = pair ? wk.tile_end(w, per_tile, U) : wk.j1;
             float m = -SPLA_INF, l = 0.f;
-            for (int j = wk.j0; j < e; ++j) {
-                const int bar = pair ? w : 2 + (sc & 1), buf = bar & 1;
-                ok = tc_wait(&nt->s_full[bar], (pair ? pc : sc >> 1) & 1, a.status);
+            for (int j = first_j; j < e; j += by, ++sc) {
+                ok = tc_wait(&nt->s_full[w], sc & 1, a.status);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (warp_live) {
                     tcf_after();
-                    const uint32_t tS = tmem + 128 * buf + lanes;
+                    const uint32_t tS = tmem + 128 * w + lanes;
                     float s[128];
                     tm_ld128(tS, s);
                     if ((int64_t)(j + 1) * kTcTile > lo_pos + 1) {
@@ -578,12 +581,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2((m - top) * a.sl2) : 1.f;
                         l *= f;
-                        if (!pair && j > wk.j0) {
-                            // the product of the step before may still be running
-                            ok = tc_wait(&nt->o_done[2 + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1, a.status);
-                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                            tcf_after();
-                        }
+                        // (the product of this stream's last step is done: S came after it)
 #pragma unroll
                         for (int i = 0; i < D; i += 32) {
                             float o[32];
@@ -618,42 +616,65 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     tcf_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&nt->p_full[bar]);
-                if (pair) ++pc;
-                else ++sc;
+                if (lane == 0) mbar_arrive(&nt->p_full[w]);
             }
             if (!ok) break;
             // ---- this segment's sums
             const bool whole = wk.j0 == 0 && wk.j1 == wk.T;
-            const int steps = max(0, e - wk.j0);
-            if (steps > 0) {
-                // one tile: the products alternate between two barriers, since the one before
-                // the last may still be running here (never more: the last S was issued
-                // after the product two steps back)
-                ok = pair ? tc_wait(&nt->o_done[w], oc & 1, a.status)
-                          : tc_wait(&nt->o_done[2 + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1, a.status);
+            const bool steps = first_j < e;
+            if (steps) {
+                ok = tc_wait(&nt->o_done[w], oc & 1, a.status);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                if (pair) ++oc;
+                ++oc;
                 tcf_after();
             }
+            // One tile with two streams: stream 0 takes both sums to the result. They stand in
+            // the same lanes of tensor memory.
+            const bool join = !pair && wk.j1 - wk.j0 > 1;
+            float m2 = m == -SPLA_INF ? -SPLA_INF : m * a.sl2, f0 = 1.f, f1 = 0.f;
+            if (join && w == 1) {
+                nt->m1[r] = m2;
+                nt->l1[r] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&nt->m_full);
+                ok = tc_wait(&nt->m_empty, mc & 1, a.status);
+            } else if (join) {
+                ok = tc_wait(&nt->m_full, mc & 1, a.status);
+                const float n2 = nt->m1[r], l1 = nt->l1[r], M = fmaxf(m2, n2);
+                // no tokens: no part; nothing but NaN logits: NaN
+                f0 = m2 == -SPLA_INF ? (l == l ? 0.f : l) : ex2(m2 - M);
+                f1 = n2 == -SPLA_INF ? (l1 == l1 ? 0.f : l1) : ex2(n2 - M);
+                l = (f0 != 0.f ? l * f0 : 0.f) + (f1 != 0.f ? l1 * f1 : 0.f);
+                m2 = M;
+            }
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            mc += join;
+            tcf_after();
             // a unit cut by this run's end starts a partial 1 unless it began before the run
             const int slot = wk.j0 == 0 ? 1 : 0;
             float* part = reinterpret_cast<float*>(a.ws + kCutBytes) +
                           ((int64_t)blockIdx.x * 2 + slot) * part_floats(D);
-            const int row = w * 128 + r;
-            if (warp_live) {
-                const bool notes = steps > 0 && nt->nf_seg == seg;
+            const int row = (pair ? w * 128 : 0) + r;
+            if (warp_live && (pair || w == 0)) {
+                const bool notes = steps && nt->nf_seg == seg;
                 const float inv = 1.f / l;
                 const int64_t orow = ((int64_t)(wk.b * (int64_t)a.max_new + tok) * c.hq +
                                       wk.h * G + r % G);
 #pragma unroll
                 for (int i = 0; i < D; i += 32) {
                     float o[32];
-                    if (steps > 0) {
+                    if (steps) {
                         tm_ld32(tO + i, o);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                    }
+                    if (join) {
+                        float y[32];
+                        tm_ld32(tO + 128 + i, y);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = (f0 != 0.f ? o[k] * f0 : 0.f) + (f1 != 0.f ? y[k] * f1 : 0.f);
                     }
                     if (notes) {
                         for (int k = 0; k < 32; ++k)
@@ -676,7 +697,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     }
                     __syncwarp();                       // the next load is the whole warp's
                 }
-                const float m2 = m == -SPLA_INF ? -SPLA_INF : m * a.sl2;
                 if (live && whole) {
                     if (a.lse) a.lse[orow] = (m2 + log2f(l)) * 0.69314718055994531f;
                 } else if (live) {
@@ -685,7 +705,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 }
             }
             wk.note_cut(cut, U, G, nt->run);
+            tcf_before();
             __syncwarp();
+            if (join && w == 0 && lane == 0) mbar_arrive(&nt->m_empty);
             if (lane == 0) {
                 __threadfence_block();
                 atomicAdd(&nt->epi, 1);
