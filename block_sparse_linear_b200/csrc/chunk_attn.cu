@@ -27,7 +27,10 @@
 namespace spla {
 
 constexpr int kFKT = 64;                            // tokens of a step
-using FWalk = Walk<kFKT>;
+struct FCost {                                      // a unit's start and end take a step's time
+    static constexpr int kPair = 1, kOne = 1, kUnit = 1;
+};
+using FWalk = Walk<kFKT, FCost>;
 
 template <int D, int WM>
 struct FShape {
@@ -90,16 +93,19 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp % WM, wn = warp / WM, g = lane >> 2, t = lane & 3;
     const int G = c.group, U = kRows / G;
-    if (tid == 0) start.left = 0;
+    if (tid == 0) {
+        start.j = 0;
+        start.F = start.end = 0;
+    }
     pdl_trigger();
     pdl_wait();
-    find_run<kFKT, kFThreads>(c, a, U, scan, &start, &run);
+    find_run<kFKT, FCost, kFThreads>(c, a, U, U, scan, &start, &run);
     FWalk wk = start;
     ChunkCut cut = {};
     auto ktile = [&](int s) { return f_smem + s * 2 * S::kTile; };
     auto vtile = [&](int s) { return f_smem + s * 2 * S::kTile + S::kTile; };
 
-    while (wk.next(c, a, U)) {
+    while (wk.next(c, a, U, U)) {
         const int tok0 = wk.qb * U;
         const int base_pos = wk.L - wk.n;
         // this lane's two rows

@@ -11,9 +11,10 @@
 // unit is one (sequence, KV head, block of U query tokens).
 //
 // Split. Every unit takes T = ceil(visible tokens / KT) steps over KT-token tiles of K and
-// V. All units' steps in a row, sum T = W of them, are cut into equal runs of
-// C = ceil(W / gridDim) steps, one per CTA (one CTA per SM), whatever the lengths: a
-// single long sequence, a ragged batch and many short prompts all fill the GPU evenly.
+// V. All units' steps in a row, each with its cost (Cost: a step of a unit of two query
+// tiles, of one, and what starting a unit takes), are cut into runs of equal cost, one per
+// CTA (one CTA per SM), whatever the lengths: a single long sequence, a ragged batch and
+// many short prompts all fill the GPU evenly.
 // A unit that lies within one run is finished there; one that is cut leaves unnormalised
 // partial sums (O, l, and the maximum m they are scaled by, in log2 units), which
 // chunk_combine_kernel joins in run order, so results do not depend on timing.
@@ -71,49 +72,63 @@ __device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U)
     return sum;
 }
 
-// Steps of all of a sequence's units for one KV head.
-template <int KT>
-__device__ __forceinline__ int64_t steps_of(int32_t L, int32_t n, int U) {
-    return steps_before<KT>(L - n, (n + U - 1) / U - 1, U) + (L + KT - 1) / KT;
-}
-
-// A place in the row of all units' steps, and the walk over it that every role makes.
-template <int KT>
+// A place in the row of all units' steps, and the walk over it that every role makes. A
+// unit's step 0 stands at its place F in the row, step j at F + Cost::kUnit + j w, and a run
+// has the steps that stand in it. per_tile: query tokens of an MMA tile, U or U / 2.
+template <int KT, class Cost>
 struct Walk {
     int b, h, qb;             // unit
     int32_t L, n;             // its sequence's length and chunk
-    int j;                    // next step of the unit
-    int64_t left;             // steps left in this run
-    int j0, j1, T;            // the current segment [j0, j1) of the unit's T steps
+    int j;                    // next step of the unit; -1: the unit is done
+    int64_t F, end;           // the unit's place, this run's end
+    int j0, j1, T, w;         // the current segment [j0, j1) of the unit's T steps of cost w
 
-    __device__ __forceinline__ int units(int U) const { return (n + U - 1) / U; }
+    __device__ __forceinline__ static int units(int32_t n, int U) { return (n + U - 1) / U; }
+    // Whether the unit's queries reach past its first tile.
+    __device__ __forceinline__ bool pair(int per_tile, int U) const {
+        return (int64_t)qb * U + per_tile < n;
+    }
+    // Cost of a sequence's units before block qb, and of all of them, for one KV head.
+    __device__ __forceinline__ static int64_t cost_before(int32_t base, int32_t qb, int U) {
+        return (int64_t)Cost::kUnit * qb + Cost::kPair * steps_before<KT>(base, qb, U);
+    }
+    __device__ __forceinline__ static int64_t cost_of(int32_t L, int32_t n, int per_tile, int U) {
+        const int q = units(n, U) - 1;
+        const int w = (int64_t)q * U + per_tile < n ? Cost::kPair : Cost::kOne;
+        return cost_before(L - n, q, U) + Cost::kUnit + (int64_t)w * ((L + KT - 1) / KT);
+    }
     // Next segment of this run; false at its end.
-    __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int U) {
-        if (left <= 0) return false;
+    __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int per_tile,
+                                         int U) {
         if (j < 0) {                                  // the last unit is done: go to the next
+            F += Cost::kUnit + (int64_t)T * w;
             j = 0;
-            if (++qb >= units(U)) {
+            if (F < end && ++qb >= units(n, U)) {
                 qb = 0;
                 if (++h >= c.hkv) {
                     h = 0;
                     n = 0;
                     while (n == 0) {
-                        if (++b >= c.batch) return false;
+                        if (++b >= c.batch) {
+                            end = F;
+                            return false;
+                        }
                         chunk_of(c, a, b, &L, &n, false);
                     }
                 }
             }
         }
+        if (F >= end) return false;
         T = (int)((L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + KT - 1) / KT);
+        w = pair(per_tile, U) ? Cost::kPair : Cost::kOne;
+        const int64_t room = end - F - Cost::kUnit;
         j0 = j;
-        j1 = (int)min((int64_t)T, j0 + left);
-        left -= j1 - j0;
+        j1 = room <= w ? 1 : room >= (int64_t)T * w ? T : (int)(((uint32_t)room + w - 1) / w);
+        j1 = min(j1, T);
+        if (j0 >= j1) return false;
         j = j1 < T ? j1 : -1;
+        if (j > 0) end = F;                           // the run is over after this segment
         return true;
-    }
-    // Whether the unit's queries reach past its first tile.
-    __device__ __forceinline__ bool pair(int per_tile, int U) const {
-        return (int64_t)qb * U + per_tile < n;
     }
     // Steps that query tile w of the unit takes part in end here.
     __device__ __forceinline__ int tile_end(int w, int per_tile, int U) const {
@@ -123,10 +138,10 @@ struct Walk {
         return min(j1, (int)((last + KT - 1) / KT));
     }
     // For the join: what the current segment leaves when its unit starts in it and goes on
-    // past this run of C steps.
+    // past this run of length C.
     __device__ __forceinline__ void note_cut(ChunkCut& cut, int U, int G, int64_t C) const {
         if (j0 != 0 || j1 >= T) return;
-        cut.parts = 1 + (int)((T - j1 + C - 1) / C);
+        cut.parts = 1 + (int)((F + Cost::kUnit + (int64_t)(T - 1) * w) / C) - (int)blockIdx.x;
         cut.rows = (int)min((int64_t)U, n - (int64_t)qb * U) * G;
         cut.b = b;
         cut.h = h;
@@ -135,11 +150,13 @@ struct Walk {
 };
 
 // This CTA's place, by all NT threads of it: contiguous sequences per thread, a scan over
-// the CTA. *start (start->left = 0 beforehand) and *run are for all after the call; scan
-// holds NT / 32 values. Two barriers.
-template <int KT, int NT>
-__device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a, int U,
-                                         int64_t* scan, Walk<KT>* start, int64_t* run) {
+// the CTA. *start (an empty run beforehand) and *run, its length, are for all after the
+// call; scan holds NT / 32 values. Two barriers.
+template <int KT, class Cost, int NT>
+__device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a, int per_tile,
+                                         int U, int64_t* scan, Walk<KT, Cost>* start,
+                                         int64_t* run) {
+    using W_ = Walk<KT, Cost>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
     int64_t mine = 0;
@@ -148,7 +165,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         if (b >= c.batch) break;
         int32_t L, n;
         chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
-        if (n) mine += c.hkv * steps_of<KT>(L, n, U);
+        if (n) mine += c.hkv * W_::cost_of(L, n, per_tile, U);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -163,34 +180,43 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         if (w < warp) upto += scan[w];
         W += scan[w];
     }
-    const int64_t C = W <= INT32_MAX ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
-                                     : (W + gridDim.x - 1) / gridDim.x;
+    // a run has the place of a step at least: steps stand no further apart
+    const int64_t C = max(W <= INT32_MAX ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
+                                         : (W + gridDim.x - 1) / gridDim.x,
+                          (int64_t)(Cost::kUnit + max(Cost::kPair, Cost::kOne)));
     const int64_t f0 = (int64_t)blockIdx.x * C;
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
         int64_t at = f0 - (upto - mine);
-        Walk<KT> w;
+        W_ w;
         for (int i = 0; i < per; ++i) {
             w.b = tid * per + i;
             chunk_of(c, a, w.b, &w.L, &w.n, false);
             if (!w.n) continue;
             const int32_t base = w.L - w.n;
-            const int64_t one = steps_of<KT>(w.L, w.n, U);
+            const int64_t one = W_::cost_of(w.L, w.n, per_tile, U);
             if (at >= one * c.hkv) {
                 at -= one * c.hkv;
                 continue;
             }
             for (w.h = 0; at >= one; ++w.h) at -= one;
-            int32_t lo = 0, hi = w.units(U) - 1;
+            int32_t lo = 0, hi = W_::units(w.n, U) - 1;
             while (lo < hi) {
                 const int32_t mid = (lo + hi + 1) / 2;
-                if (steps_before<KT>(base, mid, U) <= at) lo = mid;
+                if (W_::cost_before(base, mid, U) <= at) lo = mid;
                 else hi = mid - 1;
             }
             w.qb = lo;
-            w.j = (int)(at - steps_before<KT>(base, lo, U));
+            at -= W_::cost_before(base, lo, U);       // how far into the unit the run starts
+            w.T = (int)((base + min((int64_t)(lo + 1) * U, (int64_t)w.n) + KT - 1) / KT);
+            w.w = w.pair(per_tile, U) ? Cost::kPair : Cost::kOne;
+            // the first step at or past that place, or the next unit
+            const int64_t past = at - Cost::kUnit;
+            w.j = at == 0 ? 0 : past <= w.w ? 1 : (int)(((uint32_t)past + w.w - 1) / w.w);
+            if (w.j >= w.T) w.j = -1;
             break;
         }
-        w.left = min(C, W - f0);
+        w.F = f0 - at;
+        w.end = min(f0 + C, W);
         *start = w;
         *run = C;
     }

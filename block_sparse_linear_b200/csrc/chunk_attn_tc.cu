@@ -199,7 +199,12 @@ __device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* ba
         : "memory");
 }
 
-using TcWalk = Walk<kTcTile>;
+// Measured: a step of a pair of tiles 1.45 times one of a single tile (prefill against
+// decode); a unit's start and end two of the latter.
+struct TcCost {
+    static constexpr int kPair = 3, kOne = 2, kUnit = 4;
+};
+using TcWalk = Walk<kTcTile, TcCost>;
 
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
@@ -279,7 +284,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         prefetch_tmap(&tv);
         nt->nf_seg = -1;
         nt->epi = 0;
-        nt->start.left = 0;
+        nt->start.j = 0;
+        nt->start.F = nt->start.end = 0;
     }
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
@@ -290,7 +296,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     pdl_trigger();
 
     tcf_before();
-    find_run<kTcTile, kTcThreads>(c, a, U, nt->scan, &nt->start, &nt->run);
+    find_run<kTcTile, TcCost, kTcThreads>(c, a, per_tile, U, nt->scan, &nt->start, &nt->run);
     tcf_after();
     const uint32_t tmem = nt->tmem;
     TcWalk wk = nt->start;
@@ -303,7 +309,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         bool ok = true;
         const int32_t none = (int32_t)((int64_t)c.num_phys * c.hkv * c.bs);   // reads as zeros
         const int upb = c.bs / 64;                      // 64-token rows of a page
-        while (ok && wk.next(c, a, U)) {
+        while (ok && wk.next(c, a, per_tile, U)) {
             const int32_t* row = c.table + (int64_t)wk.b * c.mbp;
             const int nu = (wk.L + 63) / 64;            // 64-token rows the sequence holds
             int32_t ys = none;
@@ -464,7 +470,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             __syncwarp();
             return true;
         };
-        while (ok && wk.next(c, a, U)) {
+        while (ok && wk.next(c, a, per_tile, U)) {
             const int qi = seg % S::kQBufs, qt = qi * S::kQTiles;
             uint64_t* q_empty = &nt->q_empty[qi];
             if (!(ok = wait(&nt->q_full[qi], (seg / S::kQBufs) & 1))) break;
@@ -541,7 +547,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         int seg = 0;
         bool ok = true;
         ChunkCut cut = {};
-        while (ok && wk.next(c, a, U)) {
+        while (ok && wk.next(c, a, per_tile, U)) {
             // a pair: stream w is query tile w, every step; one tile: every other step of it
             const bool pair = kTwo && wk.pair(per_tile, U);
             const int t0 = wk.qb * U + (pair ? w * per_tile : 0);

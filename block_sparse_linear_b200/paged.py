@@ -23,14 +23,18 @@ from . import _lib
 
 BlockPlan = namedtuple("BlockPlan", "n_granted lens_after positions slots free_count")
 
-def _elsewhere(device):
-    """Whether another device is current than the tensors' (launches go to the current one)."""
-    return torch.cuda.current_device() != device.index
+def _elsewhere(device, stream):
+    """Whether the call has to be made within _at: another device is current than the tensors'
+    (launches go to the current one), or a stream is named (tensors made here are to be
+    allocated and filled on it)."""
+    return stream is not None or torch.cuda.current_device() != device.index
 
 
-def _stream(device, stream):
-    if stream is not None:
-        return stream.cuda_stream
+def _at(device, stream):
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+
+
+def _stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)   # the handle without an object
 
 
@@ -95,9 +99,9 @@ class SplaBlockPool:
         shape = (b,)
         _need(context_lens, "context_lens", torch.int32, shape, dev)
         _need(n_new, "n_new", torch.int32, shape, dev)
-        if _elsewhere(dev):
-            with torch.cuda.device(dev):
-                return self.plan(context_lens, n_new, max_new, rows, commit, stream)
+        if _elsewhere(dev, stream):
+            with _at(dev, stream):
+                return self.plan(context_lens, n_new, max_new, rows, commit)
         # one allocation for the counts
         granted, after, left = n_new.new_empty(2 * b + 1).split((b, b, 1))
         if commit:
@@ -108,7 +112,7 @@ class SplaBlockPool:
             slots = n_new.new_empty((b, max_new), dtype=torch.int64)
         _lib.spla_block_plan(self.c, context_lens.data_ptr(), n_new.data_ptr(), max_new,
                              granted.data_ptr(), after.data_ptr(), _ptr(pos), _ptr(slots),
-                             left.data_ptr(), self.dev_status.data_ptr(), _stream(dev, stream))
+                             left.data_ptr(), self.dev_status.data_ptr(), _stream(dev))
         return BlockPlan(granted, after, pos, slots, left)
 
     def release(self, keep_lens, context_lens, stream=None) -> None:
@@ -117,11 +121,11 @@ class SplaBlockPool:
         dev = self.device
         _need(keep_lens, "keep_lens", torch.int32, (self.batch,), dev)
         _need(context_lens, "context_lens", torch.int32, (self.batch,), dev)
-        if _elsewhere(dev):
-            with torch.cuda.device(dev):
-                return self.release(keep_lens, context_lens, stream)
+        if _elsewhere(dev, stream):
+            with _at(dev, stream):
+                return self.release(keep_lens, context_lens)
         _lib.spla_block_release(self.c, keep_lens.data_ptr(), context_lens.data_ptr(),
-                                self.dev_status.data_ptr(), _stream(dev, stream))
+                                self.dev_status.data_ptr(), _stream(dev))
 
     def status(self) -> int:
         """Device-detected fault bits (synchronises)."""
@@ -143,9 +147,9 @@ def chunk_attention(owner, q, n_new, out=None, lse=None, lens=None, stream=None)
         _need(lens, "lens", torch.int32, (b,), dev)
         c = _lib.spla_cache.from_buffer_copy(c)
         c.context_lens = lens.data_ptr()
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return chunk_attention(owner, q, n_new, out, lse, lens, stream)
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return chunk_attention(owner, q, n_new, out, lse, lens)
     if out is None:
         out = torch.zeros_like(q)
     else:
@@ -158,7 +162,7 @@ def chunk_attention(owner, q, n_new, out=None, lse=None, lens=None, stream=None)
     ws = owner._chunk_ws
     _lib.spla_chunk_attention(p, c, q.data_ptr(), n_new.data_ptr(), T, out.data_ptr(),
                               _ptr(lse), ws.data_ptr(), ws.numel(), owner.dev_status.data_ptr(),
-                              _stream(dev, stream))
+                              _stream(dev))
     return out
 
 
@@ -248,10 +252,10 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
         _need(k_gamma, "k_gamma", torch.float32, (d,), dev)
     if (slots is None) != (kv is None) or (kv is not None and (k_out is not None or v_out is not None)):
         raise ValueError("kv and slots go together, and without k_out and v_out")
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
             return qk_norm_rope(cfg, q, k, v, positions, inv_freq, q_gamma, k_gamma, eps, interleaved,
-                                q_out, k_out, v_out, kv, slots, dev_status, stream)
+                                q_out, k_out, v_out, kv, slots, dev_status)
     if q_out is None:
         q_out = torch.zeros((rows, hq, d), dtype=dt, device=dev)
     else:
@@ -276,5 +280,5 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
     _lib.spla_qk_norm_rope(cfg.params(), q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, rows,
                            positions.data_ptr(), _ptr(inv_freq), rot, interleaved, _ptr(q_gamma),
                            _ptr(k_gamma), eps, q_out.data_ptr(), kp.data_ptr(), _ptr(vp),
-                           _ptr(slots), phys, _ptr(dev_status), _stream(dev, stream))
+                           _ptr(slots), phys, _ptr(dev_status), _stream(dev))
     return q_out if kv is not None else (q_out, k_out, v_out)
