@@ -770,7 +770,7 @@ spla_status spla_qk_norm_rope(const spla_params* params, const void* q, int64_t 
     a.hkv = (int)hkv;
     a.rot = rot_dim;
     a.interleaved = interleaved != 0;
-    a.bs = params->block_size;
+    a.lg_bs = params->block_size == 64 ? 6 : 7;
     cudaError_t err = launch_norm_rope(a, params->head_dim, params->dtype, (cudaStream_t)stream);
     return err == cudaSuccess ? SPLA_OK : cuda_fail(err);
 }

@@ -117,7 +117,7 @@ struct RopeArgs {
     int32_t* status;
     int64_t rows, num_slots;
     float eps;
-    int hq, hkv, rot, interleaved, bs;
+    int hq, hkv, rot, interleaved, lg_bs;
 };
 
 // Partial record of one decode CTA for one query head:

@@ -6,20 +6,50 @@
 // the head and the values pass through. Queries go out as rows; keys and values either
 // as rows (the append call's input) or straight into their pages by slot.
 //
-// Each element is read once and written once, so HBM bounds it: a group of d/16 lanes
-// holds one head, 16 elements a lane, as two 16-byte (bf16) loads whose positions are
-// chosen so that every rotated pair lies within one lane: no shared memory and no second
-// read for the partner, and the group's lanes still cover whole 128-byte lines.
+// Each element is read once and written once, so HBM bounds it, with the instructions per
+// element close behind: a group of d/16 lanes holds one head, 16 elements a lane, as two
+// 16-byte (bf16) loads whose positions are chosen so that every rotated pair lies within
+// one lane, and the group's lanes still cover whole 128-byte lines. A warp takes rows one
+// after another with two heads a lane in flight and no barrier wider than itself; scales,
+// cosines and sines are folded into four factors per pair once a row, and the arithmetic is
+// on pairs of fp32 (two to an instruction). With the arithmetic left out the same accesses
+// take 287 us for 65536 rows of 32 + 8 + 8 heads (5.6 TB/s); the kernel takes 340 us
+// (4.7 TB/s). Four heads in flight: 397 us (registers); 20 warps an SM instead of 16: 395 us
+// (spills); a CTA-wide table of sines, one thread per head share: 361 us.
 // The angle is taken in 64 bits (a position near a million times a frequency near one
-// has lost five digits in 32) and reduced in turns, where the reduction is exact; its
-// sine and cosine, shared by the token's q and k heads, are made once per CTA and row
-// while the first heads' loads are in flight. Norms and rotations are fp32; the one
-// rounding is the store to the tensors' type.
+// has lost five digits in 32) and reduced in turns, where the reduction is exact; a row's
+// sines and cosines are made once, by all lanes of its warp. Norms and rotations are fp32;
+// the one rounding is the store to the tensors' type.
 #include "common.cuh"
 
 namespace spla {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeCtas = 4;                     // per SM
+
+// Two fp32 values in one 64-bit register.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_of(float x, float y) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 f2_to(f2 a) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 
 // 8 consecutive elements, as fp32 or back.
 template <typename T> struct Vec8;
@@ -60,162 +90,219 @@ template <> struct Vec8<float> {
     }
 };
 
-// Grid: ceil(rows / rows_per_cta). Dynamic shared memory: rows_per_cta * rot/2 float2.
-template <int D, typename T>
-__global__ void __launch_bounds__(kRopeThreads)
-norm_rope_kernel(const RopeArgs a, int rows_per_cta) {
-    extern __shared__ float2 cs[];               // [row][rot/2] (cos, sin)
-    constexpr int LPH = D / 16;                  // lanes of one head
-    const int64_t row0 = (int64_t)blockIdx.x * rows_per_cta;
-    const int nrow = (int)min((int64_t)rows_per_cta, a.rows - row0);
-    const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);
-    const int items = nrow * heads * LPH;
-    const int half = a.rot / 2;
-    const int lane_h = threadIdx.x % LPH;
-    // element offsets of this lane's two chunks of 8 within a head
-    int c0, c1;
-    const bool turn = 16 * lane_h < a.rot;
-    if (a.interleaved || !turn) {
-        c0 = 16 * lane_h;
-        c1 = c0 + 8;
-    } else {
-        c0 = 8 * lane_h;
-        c1 = c0 + half;
+// A lane's 16 elements as the 8 pairs they rotate in, two pairs to a register.
+template <bool kInter>
+__device__ __forceinline__ void to_pairs(const float* f, f2* a, f2* b) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = kInter ? f2_of(f[4 * e], f[4 * e + 2]) : f2_of(f[2 * e], f[2 * e + 1]);
+        b[e] = kInter ? f2_of(f[4 * e + 1], f[4 * e + 3]) : f2_of(f[8 + 2 * e], f[8 + 2 * e + 1]);
     }
-    pdl_trigger();
-    pdl_wait();
-
-    auto src_of = [&](int item, int* hd, int* r) {
-        const int hi = item / LPH;
-        *r = hi / heads;
-        *hd = hi - *r * heads;
-        const int64_t row = row0 + *r;
-        const T* p;
-        if (*hd < a.hq) p = (const T*)a.q + row * a.q_stride + (int64_t)*hd * D;
-        else if (*hd < a.hq + a.hkv)
-            p = (const T*)a.k + row * a.k_stride + (int64_t)(*hd - a.hq) * D;
-        else p = (const T*)a.v + row * a.v_stride + (int64_t)(*hd - a.hq - a.hkv) * D;
-        return p;
-    };
-
-    Vec8<T> x0, x1;
-    int hd = 0, r = 0;
-    int item = threadIdx.x;
-    if (item < items) {
-        const T* p = src_of(item, &hd, &r);
-        x0.load(p + c0);
-        x1.load(p + c1);
+}
+template <bool kInter>
+__device__ __forceinline__ void from_pairs(const f2* a, const f2* b, float* f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 x = f2_to(a[e]), y = f2_to(b[e]);
+        f[kInter ? 4 * e : 2 * e] = x.x;
+        f[kInter ? 4 * e + 2 : 2 * e + 1] = x.y;
+        f[kInter ? 4 * e + 1 : 8 + 2 * e] = y.x;
+        f[kInter ? 4 * e + 3 : 8 + 2 * e + 1] = y.y;
     }
-    for (int i = threadIdx.x; i < nrow * half; i += kRopeThreads) {
-        const int ri = i / half;
-        const double turns = (double)a.positions[row0 + ri] * a.inv_freq[i - ri * half] *
-                             0.15915494309189535;           // 1 / 2 pi
-        float s, c;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-        cs[i] = make_float2(c, s);
-    }
-    __syncthreads();
+}
 
-    // every lane of a head's group runs the same trips (items is a multiple of LPH)
-    const unsigned group = (LPH == 8 ? 0xffu : 0xfu) << ((threadIdx.x & 31) / LPH * LPH);
-    while (item < items) {
-        const int64_t row = row0 + r;
-        const int32_t pos = a.positions[row];
-        T* dst = nullptr;
-        if (pos >= 0) {
-            if (hd < a.hq) {
-                dst = (T*)a.q_out + (row * a.hq + hd) * D;
-            } else {
-                const bool is_v = hd >= a.hq + a.hkv;
-                const int h = hd - a.hq - (is_v ? a.hkv : 0);
-                T* base = (T*)(is_v ? a.v_out : a.k_out);
-                if (a.slots) {
-                    const int64_t slot = a.slots[row];
-                    if (slot >= a.num_slots) {
-                        if (lane_h == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
-                    } else if (slot >= 0) {
-                        const int64_t page = slot / a.bs;
-                        dst = base + ((page * a.hkv + h) * a.bs + (slot - page * a.bs)) * D;
-                    }
-                } else {
-                    dst = base + (row * a.hkv + h) * D;
-                }
+// What turns a lane's pairs (p, q) into the result, rstd apart: (p A - q B, q C + p E) with
+// the scales within: A = ga cos, -B = -gb sin, C = gb cos, E = ga sin.
+struct Turn {
+    f2 A[4], nB[4], C[4], E[4];
+};
+
+// One warp, heads h0, h0 + step, ... (HPT at a time) of one row: nothing, norm, rotation
+// or both. src, dst: head h at + h * the stride; dst null: a skipped row.
+template <int D, typename T, bool kInter>
+__device__ __forceinline__ void rope_heads(const T* src, T* dst, int heads, int64_t dst_head,
+                                           int h0, int step, const Turn* w, bool norm, bool turn,
+                                           bool scale, float eps, int c0, int c1, unsigned group) {
+    constexpr int LPH = D / 16;
+    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;      // heads a lane has in flight
+    for (int h = h0; __any_sync(0xffffffffu, h < heads); h += kAhead * step) {
+        Vec8<T> x[kAhead][2];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (h + u * step < heads) {
+                const T* p = src + (int64_t)(h + u * step) * D;
+                x[u][0].load(p + c0);
+                x[u][1].load(p + c1);
             }
         }
-        if (hd < a.hq + a.hkv) {
-            float f[16];
-            x0.get(f);
-            x1.get(f + 8);
-            const float* gamma = hd < a.hq ? a.q_gamma : a.k_gamma;
-            if (gamma) {
-                float ss = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
+        for (int u = 0; u < kAhead; ++u) {
+            if (h + u * step >= heads) break;
+            if (w && (norm || turn || scale)) {
+                float f[16];
+                f2 p[4], q[4];
+                x[u][0].get(f);
+                x[u][1].get(f + 8);
+                to_pairs<kInter>(f, p, q);
+                if (norm) {
+                    f2 ss = f2_mul(p[0], p[0]);
+                    ss = f2_fma(q[0], q[0], ss);
 #pragma unroll
-                for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-                const float rstd = rsqrtf(ss * (1.f / D) + a.eps);
+                    for (int e = 1; e < 4; ++e) ss = f2_fma(q[e], q[e], f2_fma(p[e], p[e], ss));
+                    const float2 s2 = f2_to(ss);
+                    float sum = s2.x + s2.y;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    f[e] *= rstd * gamma[c0 + e];
-                    f[8 + e] *= rstd * gamma[c1 + e];
-                }
-            }
-            if (turn) {
-                const float2* t = cs + r * half;
-                if (a.interleaved) {
+                    for (int o = LPH / 2; o; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
+                    const float rs = rsqrtf(sum * (1.f / D) + eps);
+                    const f2 r2 = f2_of(rs, rs);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float2 w = t[c0 / 2 + e / 2];
-                        const float u = f[e], z = f[e + 1];
-                        f[e] = u * w.x - z * w.y;
-                        f[e + 1] = z * w.x + u * w.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 w = t[c0 + e];
-                        const float u = f[e], z = f[8 + e];
-                        f[e] = u * w.x - z * w.y;
-                        f[8 + e] = z * w.x + u * w.y;
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = f2_mul(p[e], r2);
+                        q[e] = f2_mul(q[e], r2);
                     }
                 }
+                if (turn) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f2 y = f2_mul(q[e], w->nB[e]), z = f2_mul(p[e], w->E[e]);
+                        p[e] = f2_fma(p[e], w->A[e], y);
+                        q[e] = f2_fma(q[e], w->C[e], z);
+                    }
+                } else if (scale) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = f2_mul(p[e], w->A[e]);
+                        q[e] = f2_mul(q[e], w->C[e]);
+                    }
+                }
+                from_pairs<kInter>(p, q, f);
+                x[u][0].set(f);
+                x[u][1].set(f + 8);
             }
-            x0.set(f);
-            x1.set(f + 8);
-        }
-        if (dst) {
-            x0.store(dst + c0);
-            x1.store(dst + c1);
-        }
-        item += kRopeThreads;
-        if (item < items) {
-            const T* p = src_of(item, &hd, &r);
-            x0.load(p + c0);
-            x1.load(p + c1);
+            if (dst) {
+                T* o = dst + (int64_t)(h + u * step) * dst_head;
+                x[u][0].store(o + c0);
+                x[u][1].store(o + c1);
+            }
         }
     }
 }
 
+// Warp v of the grid takes rows v / split, + warps / split, ...; within a row, every
+// split-th group of 32 / LPH heads from v % split, queries, then keys, then values.
+template <int D, typename T, bool kInter>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+norm_rope_kernel(const RopeArgs a, int split) {
+    constexpr int LPH = D / 16;                  // lanes of one head
+    constexpr int HPT = 32 / LPH;                // heads side by side
+    constexpr int kAng = D / 64;                 // angles per lane
+    __shared__ __align__(16) float2 cs_all[kRopeWarps][D / 2];
+    __shared__ __align__(16) float gam[2][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2* cs = cs_all[warp];
+    const int half = a.rot / 2;
+    const int lane_h = lane % LPH;
+    // element offsets of this lane's two chunks of 8 within a head
+    const bool turn = 16 * lane_h < a.rot;
+    const int c0 = kInter || !turn ? 16 * lane_h : 8 * lane_h;
+    const int c1 = kInter || !turn ? c0 + 8 : c0 + half;
+    const unsigned group = (LPH == 8 ? 0xffu : 0xfu) << (lane / LPH * LPH);
+    pdl_trigger();
+    pdl_wait();
+    for (int i = threadIdx.x; i < D; i += kRopeThreads) {
+        gam[0][i] = a.q_gamma ? a.q_gamma[i] : 1.f;
+        gam[1][i] = a.k_gamma ? a.k_gamma[i] : 1.f;
+    }
+    double freq[kAng];                           // turns per position
+#pragma unroll
+    for (int u = 0; u < kAng; ++u)
+        freq[u] = lane + 32 * u < half ? a.inv_freq[lane + 32 * u] * 0.15915494309189535 : 0.0;
+    __syncthreads();
+
+    const int64_t vw = (int64_t)blockIdx.x * kRopeWarps + warp;
+    const int64_t rows_step = (int64_t)gridDim.x * kRopeWarps / split;
+    if (vw / split >= rows_step) return;         // (warps left over by the split)
+    const int h0 = (int)(vw % split) * HPT + lane / LPH, step = split * HPT;
+    for (int64_t row = vw / split; row < a.rows; row += rows_step) {
+        const int32_t pos = a.positions[row];
+        if (pos < 0) continue;
+        int64_t kv_at = row * a.hkv * D, kv_head = D;
+        if (a.slots) {
+            const int64_t slot = a.slots[row];
+            kv_at = -1;
+            kv_head = (int64_t)D << a.lg_bs;
+            if (slot >= a.num_slots) {
+                if (lane == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
+            } else if (slot >= 0) {
+                kv_at = (((slot >> a.lg_bs) * a.hkv << a.lg_bs) + (slot & ((1 << a.lg_bs) - 1))) * D;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kAng; ++e)
+            if (lane + 32 * e < half) {
+                const double turns = (double)pos * freq[e];
+                float sn, cn;
+                sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cn);
+                cs[lane + 32 * e] = make_float2(cn, sn);
+            }
+        __syncwarp();
+        Turn w;
+        auto tables = [&](const float* g) {
+            float t[16];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                *reinterpret_cast<float4*>(t + e) = *reinterpret_cast<const float4*>(g + c0 + e);
+                *reinterpret_cast<float4*>(t + 8 + e) = *reinterpret_cast<const float4*>(g + c1 + e);
+            }
+            to_pairs<kInter>(t, w.A, w.C);
+            if (!turn) return;
+            const float4* c4 = reinterpret_cast<const float4*>(cs + (kInter ? c0 / 2 : c0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 v = c4[e];
+                const f2 co = f2_of(v.x, v.z), si = f2_of(v.y, v.w), ns = f2_of(-v.y, -v.w);
+                w.nB[e] = f2_mul(w.C[e], ns);
+                w.E[e] = f2_mul(w.A[e], si);
+                w.A[e] = f2_mul(w.A[e], co);
+                w.C[e] = f2_mul(w.C[e], co);
+            }
+        };
+        tables(gam[0]);
+        rope_heads<D, T, kInter>((const T*)a.q + row * a.q_stride, (T*)a.q_out + row * a.hq * D, a.hq,
+                                 D, h0, step, &w, a.q_gamma != nullptr, turn,
+                                 a.q_gamma != nullptr, a.eps, c0, c1, group);
+        tables(gam[1]);
+        rope_heads<D, T, kInter>((const T*)a.k + row * a.k_stride,
+                                 kv_at >= 0 ? (T*)a.k_out + kv_at : nullptr, a.hkv, kv_head, h0,
+                                 step, &w, a.k_gamma != nullptr, turn, a.k_gamma != nullptr, a.eps,
+                                 c0, c1, group);
+        if (a.v && kv_at >= 0)
+            rope_heads<D, T, kInter>((const T*)a.v + row * a.v_stride, (T*)a.v_out + kv_at, a.hkv,
+                                     kv_head, h0, step, nullptr, false, false, false, a.eps, c0, c1,
+                                     group);
+    }
+}
+
 // ------------------------------------------------------------------ host launcher
-cudaError_t launch_norm_rope(const RopeArgs& a, int d, int dtype, cudaStream_t s) {
-    if (a.rows == 0) return cudaSuccess;
-    // rows per CTA: the sines of a row serve all of its heads whatever this is; a few
-    // rows keep every thread busy where a row has few heads
-    const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);
-    const int lanes = heads * (d / 16);
-    int per = (4 * kRopeThreads + lanes - 1) / lanes;
-    const int64_t fill = a.rows / (4 * kNumSms);      // small calls: spread over the SMs first
-    if (per > fill) per = (int)(fill < 1 ? 1 : fill);
-    if (per > 16) per = 16;
-    const int64_t ctas = (a.rows + per - 1) / per;
-    const size_t smem = (size_t)per * (a.rot / 2) * sizeof(float2);
+template <int D, typename T>
+static cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
+    const int hpt = 32 / (D / 16), trips = (a.hq + hpt - 1) / hpt;
+    // a row to a warp; with fewer rows than resident warps, several warps to a row
+    const int64_t warps = (int64_t)kNumSms * kRopeCtas * kRopeWarps;
+    int split = (int)(warps / (a.rows < warps ? a.rows : warps));
+    if (split > trips) split = trips;
+    int64_t ctas = (a.rows * split + kRopeWarps - 1) / kRopeWarps;
+    if (ctas > kNumSms * kRopeCtas) ctas = kNumSms * kRopeCtas;
     const dim3 grid((unsigned)ctas), block(kRopeThreads);
-    using B16 = __nv_bfloat16;
+    return a.interleaved ? launch_pdl(norm_rope_kernel<D, T, true>, grid, block, 0, s, a, split)
+                         : launch_pdl(norm_rope_kernel<D, T, false>, grid, block, 0, s, a, split);
+}
+
+cudaError_t launch_norm_rope(const RopeArgs& a, int d, int dtype, cudaStream_t s) {
     if (d == 128)
-        return dtype == SPLA_BF16 ? launch_pdl(norm_rope_kernel<128, B16>, grid, block, smem, s, a, per)
-                                  : launch_pdl(norm_rope_kernel<128, float>, grid, block, smem, s, a, per);
-    return dtype == SPLA_BF16 ? launch_pdl(norm_rope_kernel<64, B16>, grid, block, smem, s, a, per)
-                              : launch_pdl(norm_rope_kernel<64, float>, grid, block, smem, s, a, per);
+        return dtype == SPLA_BF16 ? launch_rope<128, __nv_bfloat16>(a, s) : launch_rope<128, float>(a, s);
+    return dtype == SPLA_BF16 ? launch_rope<64, __nv_bfloat16>(a, s) : launch_rope<64, float>(a, s);
 }
 
 }  // namespace spla
