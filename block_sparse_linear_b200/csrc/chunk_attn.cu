@@ -61,24 +61,28 @@ __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// N products with one A: the three parts of a product add to the same accumulator, so
-// they are issued N apart, small parts first.
+// N products with one A. The small parts have an accumulator of their own: the tensor core
+// cuts an accumulator's low bits at every addition, always towards zero, and so loses the
+// fewer the fewer large parts are added (the sums over many groups are fp32 additions).
 template <int N>
-__device__ __forceinline__ void mma_3tf32(float (*c)[4], const uint32_t* ah, const uint32_t* al,
+__device__ __forceinline__ void mma_3tf32(float (*hi)[4], float (*lo)[4], const float* a,
                                           const float* b0, const float* b1) {
-    uint32_t h0[N], l0[N], h1[N], l1[N];
+    uint32_t ah[4], al[4], h0[N], l0[N], h1[N], l1[N];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         split_tf32(b0[n], h0[n], l0[n]);
         split_tf32(b1[n], h1[n], l1[n]);
     }
 #pragma unroll
-    for (int n = 0; n < N; ++n) mma_tf32(c[n], al, h0[n], h1[n]);
+    for (int n = 0; n < N; ++n) mma_tf32(lo[n], al, h0[n], h1[n]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) mma_tf32(c[n], ah, l0[n], l1[n]);
+    for (int n = 0; n < N; ++n) mma_tf32(hi[n], ah, h0[n], h1[n]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) mma_tf32(c[n], ah, h0[n], h1[n]);
+    for (int n = 0; n < N; ++n) mma_tf32(lo[n], ah, l0[n], l1[n]);
 }
+constexpr int kFChain = 4;                          // products of 8 in one accumulator
 
 template <int D, int WM>
 __global__ void __launch_bounds__(FShape<D, WM>::kThreads, 1)
@@ -185,20 +189,25 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 const float* vt = vtile(s) + (wn * NT * 8) * S::kLd;
                 float x[NT][4] = {};
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k) {
-                    uint32_t ah[4], al[4];
+                for (int n = 0; n < NT; n += kGrp) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) split_tf32(q[k][e], ah[e], al[e]);
+                    for (int k0 = 0; k0 < D / 8; k0 += kFChain) {
+                        float hi[kGrp][4] = {}, lo[kGrp][4] = {};
 #pragma unroll
-                    for (int n = 0; n < NT; n += kGrp) {
-                        float b0[kGrp], b1[kGrp];
+                        for (int k = k0; k < k0 + kFChain; ++k) {
+                            float b0[kGrp], b1[kGrp];
 #pragma unroll
-                        for (int e = 0; e < kGrp; ++e) {
-                            const float* kp = kt + ((n + e) * 8 + g) * S::kLd + 8 * k + t;
-                            b0[e] = kp[0];
-                            b1[e] = kp[4];
+                            for (int e = 0; e < kGrp; ++e) {
+                                const float* kp = kt + ((n + e) * 8 + g) * S::kLd + 8 * k + t;
+                                b0[e] = kp[0];
+                                b1[e] = kp[4];
+                            }
+                            mma_3tf32<kGrp>(hi, lo, q[k], b0, b1);
                         }
-                        mma_3tf32<kGrp>(x + n, ah, al, b0, b1);
+#pragma unroll
+                        for (int e = 0; e < kGrp; ++e)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) x[n + e][z] += hi[e][z] + lo[e][z];
                     }
                 }
                 const int s0 = j * kFKT + wn * NT * 8 + 2 * t;      // token of x[0][0]
@@ -251,23 +260,27 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 l_a += sa;
                 l_b += sb;
 #pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    // A's columns t and t + 4 are tokens 2t and 2t + 1
-                    uint32_t ah[4], al[4];
-                    split_tf32(x[k][0], ah[0], al[0]);
-                    split_tf32(x[k][2], ah[1], al[1]);
-                    split_tf32(x[k][1], ah[2], al[2]);
-                    split_tf32(x[k][3], ah[3], al[3]);
-                    const float* vp = vt + (k * 8 + 2 * t) * S::kLd + g;
+                for (int n = 0; n < D / 8; n += 4) {
 #pragma unroll
-                    for (int n = 0; n < D / 8; n += 4) {
-                        float b0[4], b1[4];
+                    for (int k0 = 0; k0 < NT; k0 += kGrp) {
+                        float hi[4][4] = {}, lo[4][4] = {};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            b0[e] = vp[8 * (n + e)];
-                            b1[e] = vp[8 * (n + e) + S::kLd];
+                        for (int k = k0; k < k0 + kGrp; ++k) {
+                            // A's columns t and t + 4 are tokens 2t and 2t + 1
+                            const float p[4] = {x[k][0], x[k][2], x[k][1], x[k][3]};
+                            const float* vp = vt + (k * 8 + 2 * t) * S::kLd + g + 8 * n;
+                            float b0[4], b1[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                b0[e] = vp[8 * e];
+                                b1[e] = vp[8 * e + S::kLd];
+                            }
+                            mma_3tf32<4>(hi, lo, p, b0, b1);
                         }
-                        mma_3tf32<4>(o + n, ah, al, b0, b1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) o[n + e][z] += hi[e][z] + lo[e][z];
                     }
                 }
             }
