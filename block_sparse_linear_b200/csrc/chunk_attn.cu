@@ -10,7 +10,7 @@
 // the shared memory, and these sizes are bound by the split's own instructions and by
 // shared-memory loads, not by the tensor pipe that tcgen05 would widen.
 //
-// A CTA of 8 or 16 warps: WM of them side by side over rows (16 each), the others over the
+// A CTA of 8 warps: WM of them side by side over rows (16 each), the others over the
 // tokens of a 64-token step, chosen so that few rows (decode) still use every warp; their
 // sums meet in shared memory at the end of a segment. K and V tiles come through cp.async into a
 // two-stage ring, rows padded by 16 bytes (every fragment load is free of bank conflicts).
@@ -34,9 +34,9 @@ using FWalk = Walk<kFKT, FCost>;
 
 template <int D, int WM>
 struct FShape {
-    // Warps: 16 where a thread's rows of O and Q fit 128 registers, 8 otherwise; a warp
-    // takes 8 tokens of a step at least.
-    static constexpr int kWarps = D == 64 && WM > 1 ? 16 : 8;
+    // 8 warps of 255 registers: 16 of 128 spill the fragments, 83 us against 61 for 512
+    // tokens over 3584 (4/1 heads of 64).
+    static constexpr int kWarps = 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kWN = kWarps / WM;         // warps over the tokens
     static constexpr int kNT = kFKT / 8 / kWN;      // token groups of 8 per warp and step

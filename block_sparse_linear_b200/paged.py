@@ -75,6 +75,7 @@ class SplaBlockPool:
         self.num_phys_blocks = int(free_list.shape[0])
         self.block_size = int(block_size)
         self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._rows_like = None                  # shape and type of the row outputs
         self.c = _lib.spla_block_pool(block_table.data_ptr(), free_list.data_ptr(),
                                       free_count.data_ptr(), self.batch, self.max_blocks_per_seq,
                                       self.num_phys_blocks, self.block_size)
@@ -102,14 +103,18 @@ class SplaBlockPool:
         if _elsewhere(dev, stream):
             with _at(dev, stream):
                 return self.plan(context_lens, n_new, max_new, rows, commit)
-        # one allocation for the counts
-        granted, after, left = n_new.new_empty(2 * b + 1).split((b, b, 1))
-        if commit:
-            left = self.free_count
+        like = torch.empty_like                 # (half the host time of naming shape and type)
+        granted, after = like(n_new), like(n_new)
+        left = self.free_count if commit else like(self.free_count)
         pos = slots = None
         if rows:
-            pos = n_new.new_empty((b, max_new))
-            slots = n_new.new_empty((b, max_new), dtype=torch.int64)
+            if self._rows_like is None or self._rows_like[0].shape[1] != max_new:
+                self._rows_like = tuple(
+                    torch.empty(1, dtype=dt, device=dev).expand(b, max_new)
+                    for dt in (torch.int32, torch.int64))
+            fmt = torch.contiguous_format
+            pos = like(self._rows_like[0], memory_format=fmt)
+            slots = like(self._rows_like[1], memory_format=fmt)
         _lib.spla_block_plan(self.c, context_lens.data_ptr(), n_new.data_ptr(), max_new,
                              granted.data_ptr(), after.data_ptr(), _ptr(pos), _ptr(slots),
                              left.data_ptr(), self.dev_status.data_ptr(), _stream(dev))
