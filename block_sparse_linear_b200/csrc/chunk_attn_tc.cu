@@ -28,6 +28,7 @@
 // (the first token that holds one, by kind), and the epilogue adds them to the rows that
 // see that token.
 #include <algorithm>
+#include <atomic>
 
 #include "chunk_attn.cuh"
 
@@ -199,10 +200,11 @@ __device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* ba
         : "memory");
 }
 
-// Measured: a step of a pair of tiles 1.45 times one of a single tile (prefill against
-// decode); a unit's start and end two of the latter.
+// Measured: a step of a pair of tiles takes 1.45 times one of a single tile (prefill
+// against decode), a unit's start and end three to four of the latter (24 prompts of 61 to
+// 1500 tokens: 101 us with 7, 107 with 4, 99 with 10; a ragged decode prefers 7 or more too).
 struct TcCost {
-    static constexpr int kPair = 3, kOne = 2, kUnit = 4;
+    static constexpr int kPair = 3, kOne = 2, kUnit = 7;
 };
 using TcWalk = Walk<kTcTile, TcCost>;
 
@@ -245,7 +247,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 template <int D, bool kTwo>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -430,17 +436,24 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if ((int64_t)(j + 1) * kTcTile <= wk.L - wk.n + (int64_t)wk.qb * U + 1) return true;
             unsigned char* st = ring + (i % S::kStages) * S::kTileBytes;
             const int held = (int)min((int64_t)kTcTile, wk.L - (int64_t)j * kTcTile);
-            uint32_t any = 0;
-#pragma unroll 8
-            for (int x = lane; x < kTcTile * S::kHalves * 8; x += 32) {
-                uint4* p = reinterpret_cast<uint4*>(st) + x;
-                if (((x >> 3) & 127) >= held) {
-                    *p = make_uint4(0u, 0u, 0u, 0u);
-                } else {                                // an exponent of all ones carries out
-                    const uint4 v = *p;
-                    any |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                           ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
-                }
+            if (held < kTcTile) {                       // rows past the sequence
+                const int n16 = (kTcTile - held) * 8;
+                for (int x = lane; x < n16 * S::kHalves; x += 32)
+                    *(reinterpret_cast<uint4*>(st + (x / n16) * 16384) + held * 8 + x % n16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
+            }
+            uint32_t any = 0;                           // an exponent of all ones carries out
+            const uint4* p = reinterpret_cast<const uint4*>(st) + lane;
+#pragma unroll 1
+            for (int x = 0; x < kTcTile * S::kHalves * 8 / 32; x += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = p[(x + u) * 32];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    any |= ((v[u].x & 0x7f807f80u) + 0x00800080u) | ((v[u].y & 0x7f807f80u) + 0x00800080u) |
+                           ((v[u].z & 0x7f807f80u) + 0x00800080u) | ((v[u].w & 0x7f807f80u) + 0x00800080u);
             }
             if (__any_sync(0xffffffffu, any & 0x80008000u)) {
                 if (nt->nf_seg != seg) {
@@ -714,10 +727,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             tcf_before();
             __syncwarp();
             if (join && w == 0 && lane == 0) mbar_arrive(&nt->m_empty);
-            if (lane == 0) {
-                __threadfence_block();
-                atomicAdd(&nt->epi, 1);
-            }
+            if (lane == 0) atomicAdd(&nt->epi, 1);      // (the notes were consumed above)
             ++seg;
         }
         if (tid == 0) reinterpret_cast<ChunkCut*>(a.ws)[blockIdx.x] = cut;
@@ -732,6 +742,16 @@ template <int D, bool kTwo>
 static cudaError_t launch_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, const ChunkArgs& a, cudaStream_t s) {
     using S = TcShape<D, kTwo>;
+    // the register shares are of a launch with kTcRegs a thread: with fewer, the softmax
+    // warps would wait for registers that nobody gives back
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes f;
+        const cudaError_t e = cudaFuncGetAttributes(&f, chunk_tc_kernel<D, kTwo>);
+        if (e != cudaSuccess) return e;
+        regs.store(f.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kTcRegs) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<D, kTwo>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     if (e != cudaSuccess) return e;
