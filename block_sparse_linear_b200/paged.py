@@ -225,7 +225,7 @@ def _rows(t, name, heads, d, dtype, device):
             or t.device != device or stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{name}: expected a {dtype} [rows][{heads}][{d}] tensor on {device} "
                          "whose heads lie side by side")
-    return stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+    return stride[0] if shape[0] > 1 else heads * d
 
 
 def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=None, eps=1e-6,

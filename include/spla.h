@@ -426,7 +426,7 @@ SPLA_API spla_status spla_qk_norm_rope(const spla_params* params, const void* q,
  * token; the layers that keep full attention, beside the sparse ones.
  *   cache  : its pools, block_table and context_lens (the chunk's own tokens included)
  *            are read; blk_stats, S, z and m may be NULL. top_k, n_sink, n_local and
- *            flags of params are not used.
+ *            flags of params have to be valid and are not used.
  *   q      : [batch][max_new][Hq][d]; query t of sequence b stands at position
  *            context_lens[b] - n_new[b] + t and sees the tokens up to its own.
  *   n_new  : [batch] int32 (device), each in [0, min(max_new, context_lens[b])].
@@ -437,7 +437,11 @@ SPLA_API spla_status spla_qk_norm_rope(const spla_params* params, const void* q,
  *            256-byte aligned, no initialisation; calls that share it are ordered on the
  *            GPU (one stream, or events), captured ones too.
  * Tokens past a sequence's length, and tokens after a query's own, have no part in its
- * result, whatever their slots hold. A count or length out of range sets
+ * result, whatever their slots hold. An infinity or NaN in a value that a query sees goes
+ * into its result (an infinity may give NaN where its probability underflows); in a key or
+ * the query it may make the row NaN. Logits, softmax statistics and sums are fp32; in bf16
+ * the probabilities are rounded once for the product with V. Repeated calls give the same
+ * bits. A count or length out of range sets
  * SPLA_DEV_BAD_COUNT or SPLA_DEV_CAPACITY and that sequence's rows are not written; a
  * table entry that is not a physical block sets SPLA_DEV_BAD_BLOCK_TABLE and its tokens
  * count as zero keys and values.

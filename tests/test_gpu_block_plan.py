@@ -165,3 +165,41 @@ def test_release_refuses_bad_sequences_alone():
     pool.release(dev([0, 0, 0, 0]), d)
     assert pool.status() == _lib.SPLA_DEV_CAPACITY
     assert d.tolist() == [0, 130, 130, 0] and int(pool.free_count) == len(free) - 2
+
+
+def test_named_stream_and_replayed_graph():
+    """plan and release on a stream of their own, and captured: every replay takes the next
+    blocks and follows the lengths in place."""
+    batch, mbp, block = 5, 6, 64
+    side = torch.cuda.Stream()
+    pool = SplaBlockPool.empty(batch, mbp, batch * mbp, block)
+    lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    n = dev([64, 1, 0, 63, 65])
+    torch.cuda.synchronize()
+    want = ref.plan(pool.block_table.cpu().numpy(), pool.free_list.cpu().numpy(), batch * mbp, block,
+                    lens.cpu().numpy(), n.cpu().numpy(), 65)
+    p = pool.plan(lens, n, 65, stream=side)
+    side.synchronize()
+    for key in ("n_granted", "lens_after", "positions", "slots"):
+        np.testing.assert_array_equal(getattr(p, key).cpu().numpy(), want[key])
+    pool.release(torch.zeros_like(lens), p.lens_after, stream=side)
+    side.synchronize()
+    assert int(pool.free_count) == batch * mbp and (p.lens_after == 0).all()
+    one = torch.full((batch,), 40, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        p = pool.plan(lens, one, 40)
+        lens.copy_(p.lens_after)
+    torch.cuda.synchronize()
+    table, free, top = pool.block_table.cpu().numpy(), pool.free_list.cpu().numpy(), batch * mbp
+    L = np.zeros(batch, np.int32)
+    for _ in range(10):                                     # 400 tokens: more than the table holds
+        want = ref.plan(table, free, top, block, L, np.full(batch, 40), 40)
+        graph.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(p.slots.cpu().numpy(), want["slots"])
+        np.testing.assert_array_equal(lens.cpu().numpy(), want["lens_after"])
+        table, top, L = want["block_table"], want["free_count"], want["lens_after"]
+        assert int(pool.free_count) == top
+    assert pool.status() == _lib.SPLA_DEV_CAPACITY

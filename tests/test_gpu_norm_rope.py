@@ -147,3 +147,19 @@ def test_overlapping_outputs_are_refused():
     q, k, v = buf[:, :4], buf[:, 4:5], buf[:, 5:]
     with pytest.raises(SplaError):
         qk_norm_rope(cfg, q, k, v, pos, q_out=buf.view(-1)[:4 * 4 * 64])
+
+
+def test_one_row_of_any_stride_and_a_named_stream():
+    """A single row's stride says nothing; tensors made by a call on a named stream belong to
+    it."""
+    cfg = cfg_of(4, 1, 64, "bf16")
+    base = torch.randn(2000, device="cuda").bfloat16()
+    q = base.as_strided((1, 4, 64), (3, 64, 1))
+    k = base.as_strided((1, 1, 64), (7, 5, 1), 512)
+    pos = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    want = qk_norm_rope(cfg, q.contiguous(), k.contiguous(), None, pos, freqs(64))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = qk_norm_rope(cfg, q, k, None, pos, freqs(64), stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
