@@ -65,6 +65,7 @@ __device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U)
     // every r-th block of a class adds a step
     const int lg = 31 - __clz(KT / U), r = 1 << lg;
     int64_t sum = 0;
+#pragma unroll 1
     for (int p = 0; p < r; ++p) {
         const int64_t k = (qb - p + r - 1) >> lg;
         sum += k * ((base + (p + 1) * U + KT - 1) / KT) + k * (k - 1) / 2;
@@ -108,6 +109,7 @@ struct Walk {
                 if (++h >= c.hkv) {
                     h = 0;
                     n = 0;
+#pragma unroll 1
                     while (n == 0) {
                         if (++b >= c.batch) {
                             end = F;
@@ -160,6 +162,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
     int64_t mine = 0;
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= c.batch) break;
@@ -176,6 +179,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     if (lane == 31) scan[warp] = upto;
     __syncthreads();
     int64_t W = 0;
+#pragma unroll 4
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) upto += scan[w];
         W += scan[w];
@@ -188,6 +192,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
         int64_t at = f0 - (upto - mine);
         W_ w;
+#pragma unroll 1
         for (int i = 0; i < per; ++i) {
             w.b = tid * per + i;
             chunk_of(c, a, w.b, &w.L, &w.n, false);
@@ -198,8 +203,10 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
                 at -= one * c.hkv;
                 continue;
             }
+#pragma unroll 1
             for (w.h = 0; at >= one; ++w.h) at -= one;
             int32_t lo = 0, hi = W_::units(w.n, U) - 1;
+#pragma unroll 1
             while (lo < hi) {
                 const int32_t mid = (lo + hi + 1) / 2;
                 if (W_::cost_before(base, mid, U) <= at) lo = mid;

@@ -53,7 +53,7 @@ struct TcShape {
     static constexpr int kHalves = D / 64;                   // 64-dimension boxes across a row
     static constexpr int kTileBytes = kTcTile * D * 2;       // a K, V or Q tile
     static constexpr int kBox = 8192;                        // 64 tokens x 64 dims
-    static constexpr int kCtl = 3072;                        // barriers and notes
+    static constexpr int kCtl = 3008;                        // barriers and notes
     // Query tiles of two units where they fit beside the ring: short units then follow one
     // another without a wait for their queries.
     static constexpr int kQBufs = D == 64 ? 2 : 1;
@@ -222,19 +222,15 @@ struct TcNotes {                              // control block in shared memory
     int32_t first[3][128];                    // first token with +inf, -inf, NaN, per dimension
     float m1[128], l1[128];
 };
-static_assert(sizeof(TcNotes) <= 3072, "control block");
+static_assert(sizeof(TcNotes) <= 3008, "control block");
 
 // Bounded waits. A role may sit out another's whole run (thousands of steps), so the
-// bound is a time, looked at every 1024 polls, with a count over it.
-constexpr uint32_t kTcPolls = 1u << 28;
-constexpr unsigned long long kTcWaitNs = 5000000000ull;
+// bound is far: seconds at the shortest poll. (Inlined at every use: kept small.)
+constexpr uint32_t kTcPolls = 1u << 27;
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    for (uint32_t i = 1; i < kTcPolls; ++i) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kTcPolls; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 1023u) == 0 && global_ns() - t0 > kTcWaitNs) break;
-    }
     set_status(status, SPLA_DEV_TIMEOUT);
     return false;
 }
@@ -315,10 +311,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         bool ok = true;
         const int32_t none = (int32_t)((int64_t)c.num_phys * c.hkv * c.bs);   // reads as zeros
         const int upb = c.bs / 64;                      // 64-token rows of a page
+#pragma unroll 1
         while (ok && wk.next(c, a, per_tile, U)) {
             const int32_t* row = c.table + (int64_t)wk.b * c.mbp;
             const int nu = (wk.L + 63) / 64;            // 64-token rows the sequence holds
             int32_t ys = none;
+#pragma unroll 1
             for (int j = wk.j0; j < wk.j1; ++j) {
                 const int k = (j - wk.j0) & 15;
                 if (k == 0) {                           // 16 steps' page rows at a time
@@ -334,6 +332,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 }
                 const int32_t y0 = __shfl_sync(0xffffffffu, ys, 2 * k);
                 const int32_t y1 = __shfl_sync(0xffffffffu, ys, 2 * k + 1);
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     const int s = it % S::kStages;
                     if (it >= S::kStages)
@@ -362,6 +361,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     if (lane == 0) {
                         const int tiles = wk.pair(per_tile, U) ? S::kQTiles : 1;
                         mbar_arrive_expect_tx(&nt->q_full[qs], tiles * S::kTileBytes);
+#pragma unroll 1
                         for (int w = 0; w < tiles; ++w)
                             for (int x = 0; x < S::kHalves; ++x)
                                 tma_q3(qtile + (qs * S::kQTiles + w) * S::kTileBytes + x * 16384, &tq,
@@ -373,8 +373,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             ++seg;
         }
         // the copies in flight have landed before the CTA may leave
+#pragma unroll 1
         for (int i = max(0, it - S::kStages); i < it; ++i)
             mbar_wait_bounded(&nt->kv_full[i % S::kStages], (i / S::kStages) & 1);
+#pragma unroll 1
         for (int i = max(0, seg - S::kQBufs); i < seg; ++i)
             mbar_wait_bounded(&nt->q_full[i % S::kQBufs], (i / S::kQBufs) & 1);
     } else if (warp == 9) {
@@ -382,7 +384,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         constexpr uint32_t kIdS = tc_idesc(128, false), kIdO = tc_idesc(D, true);
         const uint32_t q0 = smem_u32(qtile), r0 = smem_u32(ring);
         int it = 0, seg = 0;
-        int ps[2] = {0, 0};                             // probabilities taken, per stream
+        uint32_t ps = 0;                                // parities of the probabilities awaited
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool r = __all_sync(0xffffffffu, tc_wait(bar, parity, a.status));
@@ -423,9 +425,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                            kk != 0 ? 1u : acc);
             }
         };
-        auto p_wait = [&](int w, int& count) {
-            const bool r = wait(&nt->p_full[w], count & 1);
-            ++count;
+        auto p_wait = [&](int w) {                      // ps: a phase bit per stream
+            const bool r = wait(&nt->p_full[w], (ps >> w) & 1);
+            ps ^= 1u << w;
             return r;
         };
         // V of step j is in; where some row does not see all of it, its rows past the
@@ -438,6 +440,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const int held = (int)min((int64_t)kTcTile, wk.L - (int64_t)j * kTcTile);
             if (held < kTcTile) {                       // rows past the sequence
                 const int n16 = (kTcTile - held) * 8;
+#pragma unroll 1
                 for (int x = lane; x < n16 * S::kHalves; x += 32)
                     *(reinterpret_cast<uint4*>(st + (x / n16) * 16384) + held * 8 + x % n16) =
                         make_uint4(0u, 0u, 0u, 0u);
@@ -459,17 +462,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (nt->nf_seg != seg) {
                     // the rows of the segments before have read their notes
                     const volatile int32_t* epi = &nt->epi;
-                    const unsigned long long t1 = global_ns();
-                    while (*epi < 8 * seg && global_ns() - t1 < kTcWaitNs) {}
+#pragma unroll 1
+                    for (uint32_t i = 0; *epi < 8 * seg && i < kTcPolls; ++i) {}
                     __syncwarp();
+#pragma unroll 1
                     for (int x = lane; x < 3 * 128; x += 32) nt->first[x / 128][x % 128] = 0x7fffffff;
                     if (lane == 0) nt->nf_seg = seg;
                     __syncwarp();
                 }
                 // 16-byte chunk ch of row r sits at position ch ^ (r % 8) of its 128-byte row
+#pragma unroll 1
                 for (int x = lane; x < kTcTile * S::kHalves * 8; x += 32) {
                     const int r = (x >> 3) & 127, dim0 = (x >> 10) * 64 + (((x & 7) ^ (r & 7)) << 3);
                     uint32_t* p = reinterpret_cast<uint32_t*>(st + x * 16);
+#pragma unroll 1
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t h16 = (p[e >> 1] >> (16 * (e & 1))) & 0xffffu;
                         if ((h16 & 0x7f80u) != 0x7f80u) continue;
@@ -483,6 +489,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             __syncwarp();
             return true;
         };
+#pragma unroll 1
         while (ok && wk.next(c, a, per_tile, U)) {
             const int qi = seg % S::kQBufs, qt = qi * S::kQTiles;
             uint64_t* q_empty = &nt->q_empty[qi];
@@ -492,20 +499,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (kTwo && wk.pair(per_tile, U)) {
                 const int e[2] = {wk.tile_end(0, per_tile, U), wk.tile_end(1, per_tile, U)};
                 if (!(ok = full(it))) break;
+#pragma unroll 1
                 for (int w = 0; w < 2; ++w)
-                    if (wk.j0 < e[w]) do_s(qt + w, w, it);
+                    if (wk.j0 < (w ? e[1] : e[0])) do_s(qt + w, w, it);
                 commit(&nt->kv_empty[it % S::kStages]);
                 if (nj == 1) commit(q_empty);
+#pragma unroll 1
                 for (int i = 0; i < nj && ok; ++i) {
                     const int j = wk.j0 + i, iv = it + 2 * i + 1, ik = iv + 1;
                     if (!(ok = v_wait(j, iv))) break;
                     if (i + 1 < nj && !(ok = full(ik))) break;
-#pragma unroll
+#pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
-                        if (j >= e[w]) continue;
-                        if (!(ok = p_wait(w, ps[w]))) break;
+                        const int ew = w ? e[1] : e[0];
+                        if (j >= ew) continue;
+                        if (!(ok = p_wait(w))) break;
                         do_o(w, iv, i == 0);
-                        if (j + 1 < e[w]) do_s(qt + w, w, ik);
+                        if (j + 1 < ew) do_s(qt + w, w, ik);
                         else commit(&nt->o_done[w]);
                     }
                     commit(&nt->kv_empty[iv % S::kStages]);
@@ -513,16 +523,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     if (i + 2 == nj) commit(q_empty);
                 }
             } else {
+#pragma unroll 1
                 for (int i = 0; i < 2 && i < nj && ok; ++i) {
                     if (!(ok = full(it + 2 * i))) break;
                     do_s(qt, i, it + 2 * i);
                     commit(&nt->kv_empty[(it + 2 * i) % S::kStages]);
                     if (i + 1 == nj) commit(q_empty);
                 }
+#pragma unroll 1
                 for (int i = 0; i < nj && ok; ++i) {
                     const int w = i & 1, iv = it + 2 * i + 1, ik = iv + 3;
                     if (!(ok = v_wait(wk.j0 + i, iv))) break;
-                    if (!(ok = w ? p_wait(1, ps[1]) : p_wait(0, ps[0]))) break;
+                    if (!(ok = p_wait(w))) break;
                     do_o(w, iv, i < 2);
                     if (i + 2 >= nj) commit(&nt->o_done[w]);
                     commit(&nt->kv_empty[iv % S::kStages]);
@@ -560,6 +572,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         int seg = 0;
         bool ok = true;
         ChunkCut cut = {};
+#pragma unroll 1
         while (ok && wk.next(c, a, per_tile, U)) {
             // a pair: stream w is query tile w, every step; one tile: every other step of it
             const bool pair = kTwo && wk.pair(per_tile, U);
@@ -572,6 +585,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const int first_j = wk.j0 + (pair ? 0 : w), by = pair ? 1 : 2;
             const int e = pair ? wk.tile_end(w, per_tile, U) : wk.j1;
             float m = -SPLA_INF, l = 0.f;
+#pragma unroll 1
             for (int j = first_j; j < e; j += by, ++sc) {
                 ok = tc_wait(&nt->s_full[w], sc & 1, a.status);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -601,7 +615,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         const float f = grow ? ex2((m - top) * a.sl2) : 1.f;
                         l *= f;
                         // (the product of this stream's last step is done: S came after it)
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < D; i += 32) {
                             float o[32];
                             tm_ld32(tO + i, o);
@@ -679,7 +693,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const float inv = 1.f / l;
                 const int64_t orow = ((int64_t)(wk.b * (int64_t)a.max_new + tok) * c.hq +
                                       wk.h * G + r % G);
-#pragma unroll
+#pragma unroll 1                                        // (cold code is fetched at every launch)
                 for (int i = 0; i < D; i += 32) {
                     float o[32];
                     if (steps) {
@@ -694,11 +708,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             o[k] = (f0 != 0.f ? o[k] * f0 : 0.f) + (f1 != 0.f ? y[k] * f1 : 0.f);
-                    }
-                    if (notes) {
-                        for (int k = 0; k < 32; ++k)
-                            o[k] += note_term(nt->first[0][i + k], nt->first[1][i + k],
-                                              nt->first[2][i + k], pos);
                     }
                     if (live && whole) {
                         uint4* d = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + orow * D + i);
@@ -715,6 +724,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                             d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                     __syncwarp();                       // the next load is the whole warp's
+                }
+                if (notes && live) {                    // rare: infinities and NaN that were seen
+#pragma unroll 1
+                    for (int i = 0; i < D; ++i) {
+                        const float x = note_term(nt->first[0][i], nt->first[1][i], nt->first[2][i], pos);
+                        if (x == 0.f) continue;
+                        if (whole) {
+                            __nv_bfloat16* d = (__nv_bfloat16*)a.out + orow * D + i;
+                            *d = __float2bfloat16_rn(__bfloat162float(*d) + x);
+                        } else {
+                            part[(int64_t)row * D + i] += x;
+                        }
+                    }
                 }
                 if (live && whole) {
                     if (a.lse) a.lse[orow] = (m2 + log2f(l)) * 0.69314718055994531f;
