@@ -30,7 +30,7 @@ constexpr int kFKT = 64;                            // tokens of a step
 struct FCost {                                      // a unit's start and end take a step's time
     static constexpr int kPair = 1, kOne = 1, kUnit = 1;
 };
-using FWalk = Walk<kFKT, FCost>;
+template <int WM> using FWalk = Walk<kFKT, FCost, (WM < 8)>;   // (WM < 8: one unit holds the chunk)
 
 template <int D, int WM>
 struct FShape {
@@ -92,19 +92,19 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
     constexpr int kRows = 16 * WM, kGrp = NT < 4 ? NT : 4;
     extern __shared__ __align__(16) float f_smem[];
     __shared__ int64_t scan[kFThreads / 32], run;
-    __shared__ FWalk start;
+    __shared__ FWalk<WM> start;
     __shared__ int32_t first[3][D], noted;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp % WM, wn = warp / WM, g = lane >> 2, t = lane & 3;
-    const int G = c.group, U = kRows / G;
+    const int G = c.group, lgG = G >> 1, U = kRows >> lgG;
     if (tid == 0) {
         start.j = 0;
         start.F = start.end = 0;
     }
     pdl_trigger();
     pdl_wait();
-    find_run<kFKT, FCost, kFThreads>(c, a, U, U, scan, &start, &run);
-    FWalk wk = start;
+    find_run<kFThreads>(c, a, U, U, scan, &start, &run);
+    FWalk<WM> wk = start;
     ChunkCut cut = {};
     auto ktile = [&](int s) { return f_smem + s * 2 * S::kTile; };
     auto vtile = [&](int s) { return f_smem + s * 2 * S::kTile + S::kTile; };
@@ -114,17 +114,19 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
         const int base_pos = wk.L - wk.n;
         // this lane's two rows
         const int row_a = wm * 16 + g, row_b = row_a + 8;
-        const int tok_a = tok0 + row_a / G, tok_b = tok0 + row_b / G;
+        const int tok_a = tok0 + (row_a >> lgG), tok_b = tok0 + (row_b >> lgG);
         const int pos_a = base_pos + tok_a, pos_b = base_pos + tok_b;
-        const bool warp_live = tok0 + wm * 16 / G < wk.n;
+        const bool warp_live = tok0 + (wm * 16 >> lgG) < wk.n;
         float o[D / 8][4] = {};
         float m_a = -SPLA_INF, m_b = -SPLA_INF, l_a = 0.f, l_b = 0.f;
         __syncthreads();                            // the last segment's sums have been read
+#pragma unroll 1
         for (int i = tid; i < 3 * D; i += kFThreads) first[i / D][i % D] = 0x7fffffff;
         if (tid == 0) noted = 0;
 
         const int32_t* table = c.table + (int64_t)wk.b * c.mbp;
-        auto page_of = [&](int j) { return table[j * kFKT / c.bs]; };
+        const int lg_steps = c.bs >> 7;             // steps of a page: 1 or 2
+        auto page_of = [&](int j) { return table[j >> lg_steps]; };
         auto load = [&](int j, int s, int32_t phys) {   // a step's tiles; slots past the end are zeros
             const bool good = phys >= 0 && phys < c.num_phys;
             if (!good && tid == 0) set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
@@ -147,8 +149,8 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
         float q[D / 8][4];
         {
             const float* qp = (const float*)a.q + ((int64_t)wk.b * a.max_new * c.hq + wk.h * G) * D;
-            const float* qa = qp + ((int64_t)tok_a * c.hq + row_a % G) * D + t;
-            const float* qb = qp + ((int64_t)tok_b * c.hq + row_b % G) * D + t;
+            const float* qa = qp + ((int64_t)tok_a * c.hq + (row_a & (G - 1))) * D + t;
+            const float* qb = qp + ((int64_t)tok_b * c.hq + (row_b & (G - 1))) * D + t;
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
                 q[k][0] = tok_a < wk.n ? qa[8 * k] : 0.f;
@@ -157,6 +159,7 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 q[k][3] = tok_b < wk.n ? qb[8 * k + 4] : 0.f;
             }
         }
+#pragma unroll 1
         for (int j = wk.j0; j < wk.j1; ++j) {
             const int s = (j - wk.j0) & 1;
             if (j + 1 < wk.j1) {
@@ -167,6 +170,7 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             // the chunks of V this thread fetched
+#pragma unroll 4
             for (int i = tid; i < kFKT * (D / 4); i += kFThreads) {
                 const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
                 float* p = vtile(s) + r * S::kLd + x;
@@ -174,6 +178,7 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
                 // (a maximum passes over NaN: the sum of zero products does not)
                 if (!(big < SPLA_INF) || !((v.x * 0.f + v.y * 0.f) + (v.z * 0.f + v.w * 0.f) == 0.f)) {
+#pragma unroll 1
                     for (int e = 0; e < 4; ++e)
                         if (!(fabsf(p[e]) < SPLA_INF)) {
                             const int kind = p[e] != p[e] ? 2 : p[e] < 0.f;
@@ -311,9 +316,10 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
         const bool whole = wk.j0 == 0 && wk.j1 == wk.T;
         float* part = reinterpret_cast<float*>(a.ws + kCutBytes) +
                       ((int64_t)blockIdx.x * 2 + (wk.j0 == 0 ? 1 : 0)) * part_floats(D);
+#pragma unroll 1
         for (int i = tid; i < kRows * (D / 4); i += kFThreads) {
             const int row = i / (D / 4), x = (i - row * (D / 4)) * 4;
-            const int tok = tok0 + row / G;
+            const int tok = tok0 + (row >> lgG);
             if (tok >= wk.n) break;                 // rows ascend with i
             float M = -SPLA_INF, l = 0.f;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -341,7 +347,7 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
             }
             if (whole) {
                 const float inv = 1.f / l;
-                const int64_t orow = ((int64_t)wk.b * a.max_new + tok) * c.hq + wk.h * G + row % G;
+                const int64_t orow = ((int64_t)wk.b * a.max_new + tok) * c.hq + wk.h * G + (row & (G - 1));
                 *reinterpret_cast<float4*>((float*)a.out + orow * D + x) =
                     make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
                 if (x == 0 && a.lse) a.lse[orow] = (M + log2f(l)) * 0.69314718055994531f;
@@ -378,9 +384,11 @@ chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
     // partial p is run + p's, slot 1 for the first of them and slot 0 after it
     auto part = [&](int p) { return base + ((int64_t)p * 2 + (p == 0 ? 1 : 0)) * part_floats(D); };
     float M = -SPLA_INF;
+#pragma unroll 1
     for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, part(p)[256 * D + row]);
     M = warp_max(M);
     float l = 0.f, acc[CPL] = {};
+#pragma unroll 1
     for (int p0 = 0; p0 < cut.parts; p0 += 32) {
         float w = 0.f;
         if (p0 + lane < cut.parts) {
@@ -393,6 +401,7 @@ chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
         }
         const int cnt = min(32, cut.parts - p0);
         constexpr int kBatch = 4;                   // partial rows in flight
+#pragma unroll 1
         for (int i = 0; i < cnt; i += kBatch) {
             float x[kBatch][CPL];
 #pragma unroll
@@ -413,8 +422,9 @@ chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
         }
     }
     l = warp_sum(l);
-    const int64_t orow = ((int64_t)cut.b * a.max_new + cut.t0 + row / c.group) * c.hq +
-                         cut.h * c.group + row % c.group;
+    const int lgG = c.group >> 1;
+    const int64_t orow = ((int64_t)cut.b * a.max_new + cut.t0 + (row >> lgG)) * c.hq +
+                         cut.h * c.group + (row & (c.group - 1));
     const float inv = 1.f / l;
     T* o = (T*)a.out + orow * D + lane * CPL;
     if constexpr (sizeof(T) == 4) {

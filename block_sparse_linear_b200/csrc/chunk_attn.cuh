@@ -75,8 +75,10 @@ __device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U)
 
 // A place in the row of all units' steps, and the walk over it that every role makes. A
 // unit's step 0 stands at its place F in the row, step j at F + Cost::kUnit + j w, and a run
-// has the steps that stand in it. per_tile: query tokens of an MMA tile, U or U / 2.
-template <int KT, class Cost>
+// has the steps that stand in it. per_tile: query tokens of an MMA tile, U or U / 2. kSolo:
+// no chunk of the call has more than one block of queries, of one tile (decode), which
+// leaves little of the arithmetic.
+template <int KT, class Cost, bool kSolo>
 struct Walk {
     int b, h, qb;             // unit
     int32_t L, n;             // its sequence's length and chunk
@@ -84,18 +86,21 @@ struct Walk {
     int64_t F, end;           // the unit's place, this run's end
     int j0, j1, T, w;         // the current segment [j0, j1) of the unit's T steps of cost w
 
-    __device__ __forceinline__ static int units(int32_t n, int U) { return (n + U - 1) / U; }
+    __device__ __forceinline__ static int units(int32_t n, int U) {
+        return kSolo ? 1 : (n + U - 1) / U;
+    }
     // Whether the unit's queries reach past its first tile.
     __device__ __forceinline__ bool pair(int per_tile, int U) const {
-        return (int64_t)qb * U + per_tile < n;
+        return !kSolo && (int64_t)qb * U + per_tile < n;
     }
     // Cost of a sequence's units before block qb, and of all of them, for one KV head.
     __device__ __forceinline__ static int64_t cost_before(int32_t base, int32_t qb, int U) {
+        if (kSolo) return 0;
         return (int64_t)Cost::kUnit * qb + Cost::kPair * steps_before<KT>(base, qb, U);
     }
     __device__ __forceinline__ static int64_t cost_of(int32_t L, int32_t n, int per_tile, int U) {
         const int q = units(n, U) - 1;
-        const int w = (int64_t)q * U + per_tile < n ? Cost::kPair : Cost::kOne;
+        const int w = !kSolo && (int64_t)q * U + per_tile < n ? Cost::kPair : Cost::kOne;
         return cost_before(L - n, q, U) + Cost::kUnit + (int64_t)w * ((L + KT - 1) / KT);
     }
     // Next segment of this run; false at its end.
@@ -104,7 +109,7 @@ struct Walk {
         if (j < 0) {                                  // the last unit is done: go to the next
             F += Cost::kUnit + (int64_t)T * w;
             j = 0;
-            if (F < end && ++qb >= units(n, U)) {
+            if (F < end && (kSolo || ++qb >= units(n, U))) {
                 qb = 0;
                 if (++h >= c.hkv) {
                     h = 0;
@@ -121,7 +126,8 @@ struct Walk {
             }
         }
         if (F >= end) return false;
-        T = (int)((L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + KT - 1) / KT);
+        T = kSolo ? (L + KT - 1) / KT
+                  : (int)((L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + KT - 1) / KT);
         w = pair(per_tile, U) ? Cost::kPair : Cost::kOne;
         const int64_t room = end - F - Cost::kUnit;
         j0 = j;
@@ -143,7 +149,9 @@ struct Walk {
     // past this run of length C.
     __device__ __forceinline__ void note_cut(ChunkCut& cut, int U, int G, int64_t C) const {
         if (j0 != 0 || j1 >= T) return;
-        cut.parts = 1 + (int)((F + Cost::kUnit + (int64_t)(T - 1) * w) / C) - (int)blockIdx.x;
+        // from the next run's start to the unit's last step: less than the unit's cost
+        const int64_t past = F + Cost::kUnit + (int64_t)(T - 1) * w - (int64_t)(blockIdx.x + 1) * C;
+        cut.parts = 2 + (past < C ? 0 : (int)((uint32_t)past / (uint32_t)C));
         cut.rows = (int)min((int64_t)U, n - (int64_t)qb * U) * G;
         cut.b = b;
         cut.h = h;
@@ -154,11 +162,11 @@ struct Walk {
 // This CTA's place, by all NT threads of it: contiguous sequences per thread, a scan over
 // the CTA. *start (an empty run beforehand) and *run, its length, are for all after the
 // call; scan holds NT / 32 values. Two barriers.
-template <int KT, class Cost, int NT>
+template <int NT, int KT, class Cost, bool kSolo>
 __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a, int per_tile,
-                                         int U, int64_t* scan, Walk<KT, Cost>* start,
+                                         int U, int64_t* scan, Walk<KT, Cost, kSolo>* start,
                                          int64_t* run) {
-    using W_ = Walk<KT, Cost>;
+    using W_ = Walk<KT, Cost, kSolo>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
     int64_t mine = 0;
@@ -185,8 +193,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         W += scan[w];
     }
     // a run has the place of a step at least: steps stand no further apart
-    const int64_t C = max(W <= INT32_MAX ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
-                                         : (W + gridDim.x - 1) / gridDim.x,
+    const int64_t C = max((W + kMaxRuns - 1) / kMaxRuns,
                           (int64_t)(Cost::kUnit + max(Cost::kPair, Cost::kOne)));
     const int64_t f0 = (int64_t)blockIdx.x * C;
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
@@ -205,7 +212,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
             }
 #pragma unroll 1
             for (w.h = 0; at >= one; ++w.h) at -= one;
-            int32_t lo = 0, hi = W_::units(w.n, U) - 1;
+            int32_t lo = 0, hi = W_::units(w.n, U) - 1;     // (kSolo: the block is 0)
 #pragma unroll 1
             while (lo < hi) {
                 const int32_t mid = (lo + hi + 1) / 2;

@@ -206,15 +206,16 @@ __device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* ba
 struct TcCost {
     static constexpr int kPair = 3, kOne = 2, kUnit = 7;
 };
-using TcWalk = Walk<kTcTile, TcCost>;
+template <bool kTwo> using TcWalk = Walk<kTcTile, TcCost, !kTwo>;
 
+template <bool kTwo>
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2]; // by stream
     uint64_t m_full, m_empty, fin;            // stream 1's sums for stream 0's epilogue
     int64_t scan[kTcThreads / 32];
-    TcWalk start;
+    TcWalk<kTwo> start;
     int64_t run;                              // C
     uint32_t tmem;
     int32_t nf_seg;                           // segment whose infinities and NaN are noted
@@ -222,7 +223,7 @@ struct TcNotes {                              // control block in shared memory
     int32_t first[3][128];                    // first token with +inf, -inf, NaN, per dimension
     float m1[128], l1[128];
 };
-static_assert(sizeof(TcNotes) <= 3008, "control block");
+static_assert(sizeof(TcNotes<true>) <= 3008, "control block");
 
 // Bounded waits. A role may sit out another's whole run (thousands of steps), so the
 // bound is far: seconds at the shortest poll. (Inlined at every use: kept small.)
@@ -257,10 +258,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     extern __shared__ __align__(1024) unsigned char tc_smem[];      // swizzle atoms are 1024 bytes
     unsigned char* qtile = tc_smem;
     unsigned char* ring = tc_smem + S::kQTiles * S::kQBufs * S::kTileBytes;
-    TcNotes* nt = reinterpret_cast<TcNotes*>(ring + S::kStages * S::kTileBytes);
+    TcNotes<kTwo>* nt = reinterpret_cast<TcNotes<kTwo>*>(ring + S::kStages * S::kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = c.group;
-    const int per_tile = 128 / G;                      // query tokens of a tile
+    const int G = c.group, lgG = G >> 1;               // 1, 2 or 4
+    const int per_tile = 128 >> lgG;                      // query tokens of a tile
     const int U = per_tile * S::kQTiles;
 
     if (tid == 0) {
@@ -298,10 +299,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     pdl_trigger();
 
     tcf_before();
-    find_run<kTcTile, TcCost, kTcThreads>(c, a, per_tile, U, nt->scan, &nt->start, &nt->run);
+    find_run<kTcThreads>(c, a, per_tile, U, nt->scan, &nt->start, &nt->run);
     tcf_after();
     const uint32_t tmem = nt->tmem;
-    TcWalk wk = nt->start;
+    TcWalk<kTwo> wk = nt->start;
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTcRegsLess));
@@ -310,7 +311,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         int it = 0, seg = 0;                            // ring slots filled, segments
         bool ok = true;
         const int32_t none = (int32_t)((int64_t)c.num_phys * c.hkv * c.bs);   // reads as zeros
-        const int upb = c.bs / 64;                      // 64-token rows of a page
+        const int two = c.bs >> 7;                      // whether a page has two 64-token rows
 #pragma unroll 1
         while (ok && wk.next(c, a, per_tile, U)) {
             const int32_t* row = c.table + (int64_t)wk.b * c.mbp;
@@ -323,9 +324,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     const int u = 2 * j + lane;
                     ys = none;
                     if (u < nu) {
-                        const int32_t phys = row[u / upb];
+                        const int32_t phys = row[u >> two];
                         if (phys >= 0 && phys < c.num_phys)
-                            ys = (phys * c.hkv + wk.h) * c.bs + (u % upb) * 64;
+                            ys = (phys * c.hkv + wk.h) * c.bs + (u & two) * 64;
                         else
                             set_status(a.status, SPLA_DEV_BAD_BLOCK_TABLE);
                     }
@@ -509,7 +510,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     const int j = wk.j0 + i, iv = it + 2 * i + 1, ik = iv + 1;
                     if (!(ok = v_wait(j, iv))) break;
                     if (i + 1 < nj && !(ok = full(ik))) break;
-#pragma unroll 1
+#pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         const int ew = w ? e[1] : e[0];
                         if (j >= ew) continue;
@@ -577,11 +578,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             // a pair: stream w is query tile w, every step; one tile: every other step of it
             const bool pair = kTwo && wk.pair(per_tile, U);
             const int t0 = wk.qb * U + (pair ? w * per_tile : 0);
-            const int tok = t0 + r / G;                 // query token of this row
+            const int tok = t0 + (r >> lgG);                 // query token of this row
             const bool live = tok < wk.n;
             const int pos = wk.L - wk.n + tok;
             const int lo_pos = wk.L - wk.n + t0;        // of the tile's first row
-            const bool warp_live = t0 + ((warp & 3) * 32) / G < wk.n;
+            const bool warp_live = t0 + (((warp & 3) * 32) >> lgG) < wk.n;
             const int first_j = wk.j0 + (pair ? 0 : w), by = pair ? 1 : 2;
             const int e = pair ? wk.tile_end(w, per_tile, U) : wk.j1;
             float m = -SPLA_INF, l = 0.f;
@@ -692,7 +693,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const bool notes = steps && nt->nf_seg == seg;
                 const float inv = 1.f / l;
                 const int64_t orow = ((int64_t)(wk.b * (int64_t)a.max_new + tok) * c.hq +
-                                      wk.h * G + r % G);
+                                      wk.h * G + (r & (G - 1)));
 #pragma unroll 1                                        // (cold code is fetched at every launch)
                 for (int i = 0; i < D; i += 32) {
                     float o[32];
