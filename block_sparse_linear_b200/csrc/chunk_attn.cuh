@@ -194,7 +194,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     }
     // a run has the place of a step at least: steps stand no further apart
     const int64_t C = max((W + kMaxRuns - 1) / kMaxRuns,
-                          (int64_t)(Cost::kUnit + max(Cost::kPair, Cost::kOne)));
+                          (int64_t)(Cost::kUnit + (kSolo ? Cost::kOne : max(Cost::kPair, Cost::kOne))));
     const int64_t f0 = (int64_t)blockIdx.x * C;
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
         int64_t at = f0 - (upto - mine);
