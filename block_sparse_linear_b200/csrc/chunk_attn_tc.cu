@@ -349,11 +349,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                                         64 * x, y1);
                         }
                     }
-                }
-                if (!ok) break;
-                if (j == wk.j0) {
-                    // the unit's queries, behind its first K and V: those need not wait for the
-                    // unit before to be done with its own
+                    // the unit's queries: behind its first K where their buffer is free from the
+                    // start, else behind its first V, which need not wait for the unit before to
+                    // be done with its own
+                    if (j != wk.j0 || kv != (seg >= S::kQBufs)) continue;
                     const int qs = seg % S::kQBufs;
                     if (seg >= S::kQBufs)
                         ok = tc_wait(&nt->q_empty[qs], (seg / S::kQBufs - 1) & 1, a.status);
@@ -370,6 +369,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                                        wk.b * a.max_new + wk.qb * U + w * per_tile);
                     }
                 }
+                if (!ok) break;
             }
             ++seg;
         }
