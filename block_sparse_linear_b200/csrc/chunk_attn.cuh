@@ -74,8 +74,9 @@ __device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U)
 }
 
 // A place in the row of all units' steps, and the walk over it that every role makes. A
-// unit's step 0 stands at its place F in the row, step j at F + Cost::kUnit + j w, and a run
-// has the steps that stand in it. per_tile: query tokens of an MMA tile, U or U / 2. kSolo:
+// unit's step 0 stands at its place F in the row, step j at F + start + j w, and a run has
+// the steps that stand in it. start is Cost::kUnit; with one unit per (sequence, KV head)
+// and fewer of them than runs, every run starts a unit or goes on with one, and start is 0. per_tile: query tokens of an MMA tile, U or U / 2. kSolo:
 // no chunk of the call has more than one block of queries, of one tile (decode), which
 // leaves little of the arithmetic.
 template <int KT, class Cost, bool kSolo>
@@ -85,6 +86,7 @@ struct Walk {
     int j;                    // next step of the unit; -1: the unit is done
     int64_t F, end;           // the unit's place, this run's end
     int j0, j1, T, w;         // the current segment [j0, j1) of the unit's T steps of cost w
+    int begin;                // what starting a unit costs
 
     __device__ __forceinline__ static int units(int32_t n, int U) {
         return kSolo ? 1 : (n + U - 1) / U;
@@ -93,7 +95,9 @@ struct Walk {
     __device__ __forceinline__ bool pair(int per_tile, int U) const {
         return !kSolo && (int64_t)qb * U + per_tile < n;
     }
-    // Cost of a sequence's units before block qb, and of all of them, for one KV head.
+    __device__ __forceinline__ int start() const { return kSolo ? begin : Cost::kUnit; }
+    // Cost of a sequence's units before block qb, and of all of them, for one KV head (in
+    // kSolo without the start).
     __device__ __forceinline__ static int64_t cost_before(int32_t base, int32_t qb, int U) {
         if (kSolo) return 0;
         return (int64_t)Cost::kUnit * qb + Cost::kPair * steps_before<KT>(base, qb, U);
@@ -101,13 +105,13 @@ struct Walk {
     __device__ __forceinline__ static int64_t cost_of(int32_t L, int32_t n, int per_tile, int U) {
         const int q = units(n, U) - 1;
         const int w = !kSolo && (int64_t)q * U + per_tile < n ? Cost::kPair : Cost::kOne;
-        return cost_before(L - n, q, U) + Cost::kUnit + (int64_t)w * ((L + KT - 1) / KT);
+        return cost_before(L - n, q, U) + (kSolo ? 0 : Cost::kUnit) + (int64_t)w * ((L + KT - 1) / KT);
     }
     // Next segment of this run; false at its end.
     __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int per_tile,
                                          int U) {
         if (j < 0) {                                  // the last unit is done: go to the next
-            F += Cost::kUnit + (int64_t)T * w;
+            F += start() + (int64_t)T * w;
             j = 0;
             if (F < end && (kSolo || ++qb >= units(n, U))) {
                 qb = 0;
@@ -129,7 +133,7 @@ struct Walk {
         T = kSolo ? (L + KT - 1) / KT
                   : (int)((L - n + min((int64_t)(qb + 1) * U, (int64_t)n) + KT - 1) / KT);
         w = pair(per_tile, U) ? Cost::kPair : Cost::kOne;
-        const int64_t room = end - F - Cost::kUnit;
+        const int64_t room = end - F - start();
         j0 = j;
         j1 = room <= w ? 1 : room >= (int64_t)T * w ? T : (int)(((uint32_t)room + w - 1) / w);
         j1 = min(j1, T);
@@ -150,7 +154,7 @@ struct Walk {
     __device__ __forceinline__ void note_cut(ChunkCut& cut, int U, int G, int64_t C) const {
         if (j0 != 0 || j1 >= T) return;
         // from the next run's start to the unit's last step: less than the unit's cost
-        const int64_t past = F + Cost::kUnit + (int64_t)(T - 1) * w - (int64_t)(blockIdx.x + 1) * C;
+        const int64_t past = F + start() + (int64_t)(T - 1) * w - (int64_t)(blockIdx.x + 1) * C;
         cut.parts = 2 + (past < C ? 0 : (int)((uint32_t)past / (uint32_t)C));
         cut.rows = (int)min((int64_t)U, n - (int64_t)qb * U) * G;
         cut.b = b;
@@ -169,6 +173,9 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     using W_ = Walk<KT, Cost, kSolo>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
+    // kSolo: the units are counted in the same scan, above the costs (steps of the longest
+    // sequences, 2^16, times all units, 2^23, stay below)
+    constexpr int64_t kSeq = kSolo ? 1ll << 40 : 0, kCosts = (1ll << 40) - 1;
     int64_t mine = 0;
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
@@ -176,7 +183,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         if (b >= c.batch) break;
         int32_t L, n;
         chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
-        if (n) mine += c.hkv * W_::cost_of(L, n, per_tile, U);
+        if (n) mine += c.hkv * (W_::cost_of(L, n, per_tile, U) + kSeq);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -192,9 +199,16 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         if (w < warp) upto += scan[w];
         W += scan[w];
     }
+    int begin = Cost::kUnit;
+    if (kSolo) {
+        if ((W >> 40) < kMaxRuns) begin = 0;
+        W = (W & kCosts) + begin * (W >> 40);
+        mine = (mine & kCosts) + begin * (mine >> 40);
+        upto = (upto & kCosts) + begin * (upto >> 40);
+    }
     // a run has the place of a step at least: steps stand no further apart
     const int64_t C = max((W + kMaxRuns - 1) / kMaxRuns,
-                          (int64_t)(Cost::kUnit + (kSolo ? Cost::kOne : max(Cost::kPair, Cost::kOne))));
+                          (int64_t)(begin + (kSolo ? Cost::kOne : max(Cost::kPair, Cost::kOne))));
     const int64_t f0 = (int64_t)blockIdx.x * C;
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
         int64_t at = f0 - (upto - mine);
@@ -205,7 +219,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
             chunk_of(c, a, w.b, &w.L, &w.n, false);
             if (!w.n) continue;
             const int32_t base = w.L - w.n;
-            const int64_t one = W_::cost_of(w.L, w.n, per_tile, U);
+            const int64_t one = W_::cost_of(w.L, w.n, per_tile, U) + (kSolo ? begin : 0);
             if (at >= one * c.hkv) {
                 at -= one * c.hkv;
                 continue;
@@ -224,11 +238,12 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
             w.T = (int)((base + min((int64_t)(lo + 1) * U, (int64_t)w.n) + KT - 1) / KT);
             w.w = w.pair(per_tile, U) ? Cost::kPair : Cost::kOne;
             // the first step at or past that place, or the next unit
-            const int64_t past = at - Cost::kUnit;
+            const int64_t past = at - begin;
             w.j = at == 0 ? 0 : past <= w.w ? 1 : (int)(((uint32_t)past + w.w - 1) / w.w);
             if (w.j >= w.T) w.j = -1;
             break;
         }
+        w.begin = begin;
         w.F = f0 - at;
         w.end = min(f0 + C, W);
         *start = w;
