@@ -383,35 +383,40 @@ chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
                         (int64_t)run * 2 * part_floats(D);
     // partial p is run + p's, slot 1 for the first of them and slot 0 after it
     auto part = [&](int p) { return base + ((int64_t)p * 2 + (p == 0 ? 1 : 0)) * part_floats(D); };
-    float M = -SPLA_INF;
+    // the first partials' sums are on their way with the maxima that weigh them
+    constexpr int kBatch = 8;                       // partial rows in flight
+    float x[kBatch][CPL];
+    auto fetch = [&](int p) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (p + u >= cut.parts) break;
+            const float* q = part(p + u) + (int64_t)row * D + lane * CPL;
+            if constexpr (CPL == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(q);
+            else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(q);
+        }
+    };
+    float m = -SPLA_INF, lp = 0.f;
+    auto weigh = [&](int p) {
+        m = p < cut.parts ? part(p)[256 * D + row] : -SPLA_INF;
+        lp = p < cut.parts ? part(p)[256 * D + 256 + row] : 0.f;
+    };
+    weigh(lane);
+    fetch(0);
+    float M = m;
 #pragma unroll 1
-    for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, part(p)[256 * D + row]);
+    for (int p = lane + 32; p < cut.parts; p += 32) M = fmaxf(M, part(p)[256 * D + row]);
     M = warp_max(M);
     float l = 0.f, acc[CPL] = {};
 #pragma unroll 1
     for (int p0 = 0; p0 < cut.parts; p0 += 32) {
-        float w = 0.f;
-        if (p0 + lane < cut.parts) {
-            const float* q = part(p0 + lane);
-            const float m = q[256 * D + row];
-            const float lp = q[256 * D + 256 + row];
-            // no tokens: no part; nothing but NaN logits: NaN
-            w = m == -SPLA_INF ? (lp == lp ? 0.f : lp) : ex2(m - M);
-            l += w * lp;
-        }
+        if (p0 > 0) weigh(p0 + lane);
+        // no tokens: no part; nothing but NaN logits: NaN
+        const float w = m == -SPLA_INF ? (lp == lp ? 0.f : lp) : ex2(m - M);
+        l += w * lp;
         const int cnt = min(32, cut.parts - p0);
-        constexpr int kBatch = 4;                   // partial rows in flight
 #pragma unroll 1
         for (int i = 0; i < cnt; i += kBatch) {
-            float x[kBatch][CPL];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (i + u < cnt) {
-                    const float* q = part(p0 + i + u) + (int64_t)row * D + lane * CPL;
-                    if constexpr (CPL == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(q);
-                    else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(q);
-                }
-            }
+            if (p0 + i > 0) fetch(p0 + i);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const float f = __shfl_sync(0xffffffffu, w, (i + u) & 31);
