@@ -780,6 +780,8 @@ static spla_status check_chunk(const spla_params* params, int32_t batch, int32_t
     if (st != SPLA_OK) return st;
     if (batch <= 0 || max_new < 0) return SPLA_ERR_INVALID_ARG;
     if ((int64_t)batch * max_new * params->num_q_heads > INT32_MAX) return SPLA_ERR_CAPACITY;
+    // the split counts units and their steps in one 64-bit word
+    if ((int64_t)batch * params->num_kv_heads > 1 << 22) return SPLA_ERR_CAPACITY;
     return SPLA_OK;
 }
 

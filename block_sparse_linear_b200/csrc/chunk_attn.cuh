@@ -76,9 +76,9 @@ __device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U)
 // A place in the row of all units' steps, and the walk over it that every role makes. A
 // unit's step 0 stands at its place F in the row, step j at F + start + j w, and a run has
 // the steps that stand in it. start is Cost::kUnit; with one unit per (sequence, KV head)
-// and fewer of them than runs, every run starts a unit or goes on with one, and start is 0. per_tile: query tokens of an MMA tile, U or U / 2. kSolo:
-// no chunk of the call has more than one block of queries, of one tile (decode), which
-// leaves little of the arithmetic.
+// and fewer of them than runs, every run starts a unit or goes on with one, and start is 0.
+// per_tile: query tokens of an MMA tile, U or U / 2. kSolo: no chunk of the call has more
+// than one block of queries, of one tile (decode), which leaves little of the arithmetic.
 template <int KT, class Cost, bool kSolo>
 struct Walk {
     int b, h, qb;             // unit
@@ -173,8 +173,8 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     using W_ = Walk<KT, Cost, kSolo>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
-    // kSolo: the units are counted in the same scan, above the costs (steps of the longest
-    // sequences, 2^16, times all units, 2^23, stay below)
+    // kSolo: the units, 2^22 at most, are counted in the same scan, above the costs (all
+    // their steps, 2^16 at most each, stay below)
     constexpr int64_t kSeq = kSolo ? 1ll << 40 : 0, kCosts = (1ll << 40) - 1;
     int64_t mine = 0;
 #pragma unroll 1

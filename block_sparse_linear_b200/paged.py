@@ -175,7 +175,9 @@ class SplaPagedKV:
     """Paged K and V of one full-attention layer: pools [num_phys_blocks][Hkv][B][d], the
     block table and the lengths, without the sparse path's statistics and state. The tensors
     are the caller's and are kept, not copied. block_table and context_lens may be left out
-    where only qk_norm_rope writes through it."""
+    where only qk_norm_rope writes through it. Chunk-attention calls of one object share its
+    workspace: they are made on one stream or ordered by events; layers that run side by side
+    have an object each."""
 
     def __init__(self, cfg, k_pool, v_pool, block_table=None, context_lens=None):
         _lib.load()

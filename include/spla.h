@@ -441,7 +441,8 @@ SPLA_API spla_status spla_qk_norm_rope(const spla_params* params, const void* q,
  * into its result (an infinity may give NaN where its probability underflows); in a key or
  * the query it may make the row NaN. Logits, softmax statistics and sums are fp32; in bf16
  * the probabilities are rounded once for the product with V. Repeated calls give the same
- * bits. A count or length out of range sets
+ * bits. batch * num_kv_heads is at most 2^22 and batch * max_new * num_q_heads below 2^31
+ * (SPLA_ERR_CAPACITY). A count or length out of range sets
  * SPLA_DEV_BAD_COUNT or SPLA_DEV_CAPACITY and that sequence's rows are not written; a
  * table entry that is not a physical block sets SPLA_DEV_BAD_BLOCK_TABLE and its tokens
  * count as zero keys and values.

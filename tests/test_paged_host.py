@@ -95,7 +95,7 @@ CHUNK = dict(q=FAKE, n_new=FAKE, max_new=8, out=BIG, lse=None, workspace=FAKE, w
     ({}, dict(q=None), INVALID), ({}, dict(out=None), INVALID), ({}, dict(n_new=None), INVALID),
     ({}, dict(max_new=-1), INVALID), ({}, dict(q=FAKE + 4), INVALID),
     ({}, dict(out=BIG + 2), INVALID), ({}, dict(out=FAKE + 64), INVALID),
-    ({}, dict(max_new=2 ** 28), CAPACITY),
+    ({}, dict(max_new=2 ** 28), CAPACITY), (dict(batch=2 ** 22 + 1), dict(max_new=1), CAPACITY),
     ({}, dict(workspace=None), WORKSPACE), ({}, dict(workspace=FAKE + 16), WORKSPACE),
     ({}, dict(workspace_bytes=0), WORKSPACE),
 ])
