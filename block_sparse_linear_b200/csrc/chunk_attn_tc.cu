@@ -200,22 +200,28 @@ __device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* ba
         : "memory");
 }
 
-// Measured: a step of a pair of tiles takes 1.45 times one of a single tile (prefill
-// against decode), a unit's start and end three to four of the latter (24 prompts of 61 to
-// 1500 tokens: 101 us with 7, 107 with 4, 99 with 10; a ragged decode prefers 7 or more too).
+// A step of a pair of tiles against one of a single tile, and a unit's start and end, as
+// measured: with heads of 128 a pair's step takes its products' time (2.4 us), a single
+// tile's its bytes' (1.5 us), and 7:4 beats 3:2 (12 chunks of 1 to 200 tokens over 500 to
+// 30000: 210 us against 223; no difference where all units are alike); with heads of 64
+// 3:2 beats 7:4 (12 chunks of 1 to 1000 over 100 to 8000: 114 us against 124). A unit's
+// start and end take three to four steps of a single tile (24 prompts of 61 to 1500 tokens:
+// 101 us with 7 for 3:2, 107 with 4, 99 with 10).
+template <int D>
 struct TcCost {
-    static constexpr int kPair = 3, kOne = 2, kUnit = 7;
+    static constexpr int kPair = D == 128 ? 7 : 3, kOne = D == 128 ? 4 : 2;
+    static constexpr int kUnit = D == 128 ? 14 : 7;
 };
-template <bool kTwo> using TcWalk = Walk<kTcTile, TcCost, !kTwo>;
+template <int D, bool kTwo> using TcWalk = Walk<kTcTile, TcCost<D>, !kTwo>;
 
-template <bool kTwo>
+template <int D, bool kTwo>
 struct TcNotes {                              // control block in shared memory
     uint64_t kv_full[8], kv_empty[8];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2]; // by stream
     uint64_t m_full, m_empty, fin;            // stream 1's sums for stream 0's epilogue
     int64_t scan[kTcThreads / 32];
-    TcWalk<kTwo> start;
+    TcWalk<D, kTwo> start;
     int64_t run;                              // C
     uint32_t tmem;
     int32_t nf_seg;                           // segment whose infinities and NaN are noted
@@ -223,7 +229,7 @@ struct TcNotes {                              // control block in shared memory
     int32_t first[3][128];                    // first token with +inf, -inf, NaN, per dimension
     float m1[128], l1[128];
 };
-static_assert(sizeof(TcNotes<true>) <= 3008, "control block");
+static_assert(sizeof(TcNotes<128, true>) <= 3008, "control block");
 
 // Bounded waits. A role may sit out another's whole run (thousands of steps), so the
 // bound is far: seconds at the shortest poll. (Inlined at every use: kept small.)
@@ -258,7 +264,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     extern __shared__ __align__(1024) unsigned char tc_smem[];      // swizzle atoms are 1024 bytes
     unsigned char* qtile = tc_smem;
     unsigned char* ring = tc_smem + S::kQTiles * S::kQBufs * S::kTileBytes;
-    TcNotes<kTwo>* nt = reinterpret_cast<TcNotes<kTwo>*>(ring + S::kStages * S::kTileBytes);
+    TcNotes<D, kTwo>* nt = reinterpret_cast<TcNotes<D, kTwo>*>(ring + S::kStages * S::kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = c.group, lgG = G >> 1;               // 1, 2 or 4
     const int per_tile = 128 >> lgG;                      // query tokens of a tile
@@ -302,7 +308,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     find_run<kTcThreads>(c, a, per_tile, U, nt->scan, &nt->start, &nt->run);
     tcf_after();
     const uint32_t tmem = nt->tmem;
-    TcWalk<kTwo> wk = nt->start;
+    TcWalk<D, kTwo> wk = nt->start;
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTcRegsLess));
