@@ -245,17 +245,19 @@ static bool make_input_map(CUtensorMap* m, const void* x, const CacheView& c, in
     return r == CUDA_SUCCESS;
 }
 
-// 3-D view of chunk queries [batch*max_new rows][Hq][d] bf16; box = 64 dims x the G heads of a
-// KV head x 128 / G tokens (16 KiB, the 128 rows of an MMA tile), 128B swizzle; rows past
-// the end read as zero.
+// 4-D view of chunk queries [batch][max_new][Hq][d] bf16; box = 64 dims x the G heads of a
+// KV head x 128 / G tokens of a sequence (16 KiB, the 128 rows of an MMA tile), 128B swizzle;
+// tokens past max_new read as zero.
 static bool make_query_map(CUtensorMap* m, const void* q, const CacheView& c, int32_t max_new) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)c.hq, (cuuint64_t)c.batch * max_new};
-    cuuint64_t strides[2] = {(cuuint64_t)c.d * 2, (cuuint64_t)c.hq * c.d * 2};
-    cuuint32_t box[3] = {64u, (cuuint32_t)c.group, 128u / (cuuint32_t)c.group};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
+    cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.hq, (cuuint64_t)max_new,
+                          (cuuint64_t)c.batch};
+    cuuint64_t strides[3] = {(cuuint64_t)c.d * 2, (cuuint64_t)c.hq * c.d * 2,
+                             (cuuint64_t)max_new * c.hq * c.d * 2};
+    cuuint32_t box[4] = {64u, (cuuint32_t)c.group, 128u / (cuuint32_t)c.group, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides,
                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;

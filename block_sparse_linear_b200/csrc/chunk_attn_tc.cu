@@ -191,12 +191,12 @@ __device__ __forceinline__ void tm_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tma_q3(void* dst, const void* tmap, uint64_t* bar, int32_t x,
-                                       int32_t y, int32_t z) {
+__device__ __forceinline__ void tma_q(void* dst, const void* tmap, uint64_t* bar, int32_t x,
+                                      int32_t head, int32_t tok, int32_t seq) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];"
-        :: "r"(smem_u32(dst)), "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        :: "r"(smem_u32(dst)), "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(head), "r"(tok), "r"(seq)
         : "memory");
 }
 
@@ -370,9 +370,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 #pragma unroll 1
                         for (int w = 0; w < tiles; ++w)
                             for (int x = 0; x < S::kHalves; ++x)
-                                tma_q3(qtile + (qs * S::kQTiles + w) * S::kTileBytes + x * 16384, &tq,
-                                       &nt->q_full[qs], 64 * x, wk.h * G,
-                                       wk.b * a.max_new + wk.qb * U + w * per_tile);
+                                tma_q(qtile + (qs * S::kQTiles + w) * S::kTileBytes + x * 16384, &tq,
+                                      &nt->q_full[qs], 64 * x, wk.h * G, wk.qb * U + w * per_tile,
+                                      wk.b);
                     }
                 }
                 if (!ok) break;
@@ -791,7 +791,7 @@ static cudaError_t launch_tc(const CacheView& c, const CUtensorMap& tq, const CU
     return launch_chunk_combine(c, SPLA_BF16, a, rows, s);
 }
 
-// tq: [batch * max_new][Hq][d] with boxes of 64 dims x G heads x 128 / G tokens; tk, tv:
+// tq: [batch][max_new][Hq][d] with boxes of 64 dims x G heads x 128 / G tokens; tk, tv:
 // the pools as rows of d with boxes of 64 dims x 64 tokens.
 cudaError_t launch_chunk_tc(const CacheView& c, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const ChunkArgs& a, cudaStream_t s) {
