@@ -115,6 +115,31 @@ def test_one_long_sequence(dtype, L, n_new):
     assert kv.status() == 0
 
 
+@pytest.mark.parametrize("dtype,lens", [("bf16", [200003, 90, 130001]), ("f32", [100001, 90, 65003])])
+@pytest.mark.parametrize("n_new", [1, 17])
+def test_long_runs_over_few_sequences(dtype, lens, n_new):
+    """Runs of more than 16 steps with fewer units than thread blocks: the units' starts count
+    in the split there, and a run may end one unit and begin the next."""
+    kv, q = build(32, lens, n_new, 4, 1, 64, 64, dtype)
+    out, lse = run(kv, q, [n_new] * 3)
+    check(kv, q, [n_new] * 3, lens, out, lse)
+    assert kv.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("max_new", [9, 140])
+def test_queries_past_the_counts_have_no_part(dtype, max_new):
+    """Rows of q past a sequence's count may hold anything."""
+    lens, n_new = [700, 150, 3000, 64], [5, 0, max_new, 1]
+    kv, q = build(33, lens, max_new, 8, 2, 128, 64, dtype)
+    q[0, 5:] = NAN
+    q[1] = INF
+    q[3, 1:] = -INF
+    out, lse = run(kv, q, n_new)
+    check(kv, q, n_new, lens, out, lse)
+    assert kv.status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d,block", [(64, 64), (128, 128)])
 def test_decodes_and_chunks_in_one_batch(dtype, d, block):
