@@ -329,8 +329,8 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
             for (int w = 0; w < WN; ++w) {
                 const float mw = sm[w * kRows + row], lw = sl[w * kRows + row];
                 // no tokens: no part; nothing but NaN logits: NaN
-                const float f = mw == -SPLA_INF ? (lw == lw ? 0.f : lw) : ex2(mw - M);
-                if (f == 0.f) continue;
+                if (!has_part(mw, lw)) continue;
+                const float f = mw == -SPLA_INF ? lw : ex2(mw - M);
                 const float4 v = *reinterpret_cast<const float4*>(sum + (w * kRows + row) * S::kLd + x);
                 l = fmaf(lw, f, l);
                 y.x = fmaf(v.x, f, y.x);
@@ -410,9 +410,10 @@ chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
 #pragma unroll 1
     for (int p0 = 0; p0 < cut.parts; p0 += 32) {
         if (p0 > 0) weigh(p0 + lane);
-        // no tokens: no part; nothing but NaN logits: NaN
-        const float w = m == -SPLA_INF ? (lp == lp ? 0.f : lp) : ex2(m - M);
-        l += w * lp;
+        // no tokens: no part (-1); nothing but NaN logits: NaN; else a part whatever the
+        // weight: zero times an infinity or NaN among the sums is NaN
+        const float w = !has_part(m, lp) ? -1.f : m == -SPLA_INF ? lp : ex2(m - M);
+        if (!(w < 0.f)) l += w * lp;
         const int cnt = min(32, cut.parts - p0);
 #pragma unroll 1
         for (int i = 0; i < cnt; i += kBatch) {
@@ -420,7 +421,7 @@ chunk_combine_kernel(const CacheView c, const ChunkArgs a) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const float f = __shfl_sync(0xffffffffu, w, (i + u) & 31);
-                if (i + u < cnt && f != 0.f)        // a partial without tokens has no part
+                if (i + u < cnt && !(f < 0.f))
 #pragma unroll
                     for (int e = 0; e < CPL; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
             }

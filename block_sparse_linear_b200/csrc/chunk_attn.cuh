@@ -257,6 +257,10 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     __syncthreads();
 }
 
+// Whether sums scaled by the maximum m, with probabilities that add up to l, have a part in
+// their row: not where no token was seen (m = -inf, l = 0); where all logits were NaN, l is.
+__device__ __forceinline__ bool has_part(float m, float l) { return m != -SPLA_INF || l != l; }
+
 // What infinities and NaN taken out of V (first[kind][dim]: the first token that holds
 // +inf, -inf, NaN there) add to a row at position pos.
 __device__ __forceinline__ float note_term(int32_t pinf, int32_t ninf, int32_t nan, int pos) {

@@ -672,6 +672,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             // the same lanes of tensor memory.
             const bool join = !pair && wk.j1 - wk.j0 > 1;
             float m2 = m == -SPLA_INF ? -SPLA_INF : m * a.sl2, f0 = 1.f, f1 = 0.f;
+            bool has0 = true, has1 = false;             // whether a stream has a part in the row
             if (join && w == 1) {
                 nt->m1[r] = m2;
                 nt->l1[r] = l;
@@ -681,10 +682,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             } else if (join) {
                 ok = tc_wait(&nt->m_full, mc & 1, a.status);
                 const float n2 = nt->m1[r], l1 = nt->l1[r], M = fmaxf(m2, n2);
-                // no tokens: no part; nothing but NaN logits: NaN
-                f0 = m2 == -SPLA_INF ? (l == l ? 0.f : l) : ex2(m2 - M);
-                f1 = n2 == -SPLA_INF ? (l1 == l1 ? 0.f : l1) : ex2(n2 - M);
-                l = (f0 != 0.f ? l * f0 : 0.f) + (f1 != 0.f ? l1 * f1 : 0.f);
+                // no tokens: no part; nothing but NaN logits: NaN; else a part whatever the
+                // weight, since a weight of zero makes NaN of an infinity or NaN among the sums
+                has0 = has_part(m2, l);
+                has1 = has_part(n2, l1);
+                f0 = m2 == -SPLA_INF ? l : ex2(m2 - M);
+                f1 = n2 == -SPLA_INF ? l1 : ex2(n2 - M);
+                l = (has0 ? l * f0 : 0.f) + (has1 ? l1 * f1 : 0.f);
                 m2 = M;
             }
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -714,7 +718,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         tm_ld32(tO + 128 + i, y);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            o[k] = (f0 != 0.f ? o[k] * f0 : 0.f) + (f1 != 0.f ? y[k] * f1 : 0.f);
+                            o[k] = (has0 ? o[k] * f0 : 0.f) + (has1 ? y[k] * f1 : 0.f);
                     }
                     if (live && whole) {
                         uint4* d = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + orow * D + i);

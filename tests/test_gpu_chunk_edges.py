@@ -1,0 +1,62 @@
+"""spla_chunk_attention where its parts meet: infinities and NaN in parts of little weight and
+in units that follow one another, splits of long contexts and of large batches."""
+import pytest
+import torch
+
+from .test_gpu_chunk_attention import INF, NAN, build, check, run
+
+pytestmark = pytest.mark.gpu
+
+
+def put(kv, pool, b, s, i, x):
+    """Element i (a slice: all) of every KV head's token s of sequence b."""
+    pool[kv.block_table[b, s // kv.cfg.block_size].long(), :, s % kv.cfg.block_size, i] = x
+
+
+def one_query(q):
+    """The same query in every row, so that one key can outweigh all others for all of them."""
+    q.copy_(q[:1, :1, :1].expand_as(q).clone())
+    return q[0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 5), (64, 150)])
+def test_nan_values_far_from_the_weight_of_a_long_sequence(dtype, d, n):
+    """NaN and infinities early in V, a logit hundreds of nats above all others thousands of
+    tokens later: the early tokens lie in other thread blocks' partials, whose weights are zero
+    in fp32. A NaN is seen all the same; an infinity gives itself or NaN."""
+    L = 20000
+    kv, q = build(40, [L], n, 4, 1, d, 64, dtype)
+    big = 40 * one_query(q)
+    put(kv, kv.k_pool, 0, L - 200, slice(None), big)
+    put(kv, kv.v_pool, 0, 10, 3, NAN)
+    put(kv, kv.v_pool, 0, 9000, 4, NAN)
+    out, lse = run(kv, q, [n])
+    check(kv, q, [n], [L], out, lse)
+    assert torch.isnan(out[0, :, :, 3:5]).all()
+    put(kv, kv.v_pool, 0, 700, 5, INF)
+    out, _ = run(kv, q, [n])
+    assert not torch.isfinite(out[0, :, :, 3:6]).any()
+    assert torch.isfinite(out[0, :, :, :3]).all() and torch.isfinite(out[0, :, :, 6:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_nan_values_of_little_weight_within_a_unit(dtype, n):
+    """The same in sequences of three steps, several whole ones a thread block: NaN in the step
+    of one softmax stream (or warp) and the large logit in another's, either way round."""
+    batch, L = 320, 330
+    kv, q = build(41, [L] * batch, n, 4, 1, 64, 64, dtype)
+    big = 40 * one_query(q)
+    for b in range(batch):
+        key, nan = ((20, 130), (130, 20), (20, 70), (200, 10))[b % 4]
+        put(kv, kv.k_pool, b, key, slice(None), big)
+        put(kv, kv.v_pool, b, nan, b % 64, NAN)
+    out, lse = run(kv, q, [n] * batch)
+    for b in range(0, batch, 7):
+        check(kv, q, [n if x == b else 0 for x in range(batch)], [L] * batch,
+              torch.where(torch.arange(batch, device="cuda")[:, None, None, None] == b, out, 5.0),
+              torch.where(torch.arange(batch, device="cuda")[:, None, None] == b, lse, 5.0))
+    want = torch.zeros((batch, 64), dtype=torch.bool, device="cuda")
+    want[torch.arange(batch), torch.arange(batch) % 64] = True
+    assert torch.equal(torch.isnan(out), want[:, None, None].expand_as(out))
