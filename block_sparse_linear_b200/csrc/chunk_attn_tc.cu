@@ -225,7 +225,7 @@ struct TcNotes {                              // control block in shared memory
     int64_t run;                              // C
     uint32_t tmem;
     int32_t nf_seg;                           // segment whose infinities and NaN are noted
-    int32_t epi;                              // warps past an epilogue, over all segments
+    int32_t epi[2];                           // by stream: warps past an epilogue, over all segments
     int32_t first[3][128];                    // first token with +inf, -inf, NaN, per dimension
     float m1[128], l1[128];
 };
@@ -292,7 +292,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
         nt->nf_seg = -1;
-        nt->epi = 0;
+        nt->epi[0] = nt->epi[1] = 0;
         nt->start.j = 0;
         nt->start.F = nt->start.end = 0;
     }
@@ -467,10 +467,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             }
             if (__any_sync(0xffffffffu, any & 0x80008000u)) {
                 if (nt->nf_seg != seg) {
-                    // the rows of the segments before have read their notes
-                    const volatile int32_t* epi = &nt->epi;
+                    // the rows of the segments before have read their notes, those of either
+                    // stream: in segments of one step stream 1 runs ahead
+                    const volatile int32_t* epi = nt->epi;
+                    uint32_t polls = 0;
 #pragma unroll 1
-                    for (uint32_t i = 0; *epi < 8 * seg && i < kTcPolls; ++i) {}
+                    while ((epi[0] < 4 * seg || epi[1] < 4 * seg) && ++polls < kTcPolls) {}
+                    if (polls == kTcPolls) set_status(a.status, SPLA_DEV_TIMEOUT);
                     __syncwarp();
 #pragma unroll 1
                     for (int x = lane; x < 3 * 128; x += 32) nt->first[x / 128][x % 128] = 0x7fffffff;
@@ -760,7 +763,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             tcf_before();
             __syncwarp();
             if (join && w == 0 && lane == 0) mbar_arrive(&nt->m_empty);
-            if (lane == 0) atomicAdd(&nt->epi, 1);      // (the notes were consumed above)
+            if (lane == 0) atomicAdd(&nt->epi[w], 1);      // (the notes were consumed above)
             ++seg;
         }
         if (tid == 0) reinterpret_cast<ChunkCut*>(a.ws)[blockIdx.x] = cut;

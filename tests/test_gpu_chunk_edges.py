@@ -60,3 +60,26 @@ def test_nan_values_of_little_weight_within_a_unit(dtype, n):
     want = torch.zeros((batch, 64), dtype=torch.bool, device="cuda")
     want[torch.arange(batch), torch.arange(batch) % 64] = True
     assert torch.equal(torch.isnan(out), want[:, None, None].expand_as(out))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,max_new", [(64, 1), (128, 1), (64, 20), (128, 60)])
+def test_infinities_of_units_that_follow_one_another(dtype, d, max_new):
+    """Hundreds of sequences of a step or two, several a thread block, each with an infinity or
+    NaN of its own in V: no row misses its own or has its neighbours'."""
+    batch, kinds = 700, (INF, -INF, NAN)
+    lens = [1 + (53 * b) % (128 if b % 5 else 250) for b in range(batch)]
+    n_new = [min(L, 1 + b % max_new) for b, L in enumerate(lens)]
+    kv, q = build(42, lens, max_new, 4, 2, d, 64, dtype)
+    want = torch.zeros((batch, d), device="cuda")
+    for b, (L, n) in enumerate(zip(lens, n_new)):
+        at, x = (L - n) * (b % 7) // 6, kinds[b % 3]      # a token that every query sees
+        put(kv, kv.v_pool, b, at, (11 * b) % d, x)
+        want[b, (11 * b) % d] = x
+    live = torch.arange(max_new, device="cuda")[None] < torch.tensor(n_new, device="cuda")[:, None]
+    for _ in range(5):
+        out, _ = run(kv, q, n_new)
+        got = torch.where(torch.isfinite(out), 0.0, out.float())
+        expect = torch.where(live[..., None, None], want[:, None, None], 0.0).expand_as(got)
+        assert torch.equal(got.nan_to_num(nan=7.0), expect.nan_to_num(nan=7.0))
+    assert kv.status() == 0
