@@ -477,7 +477,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     __syncwarp();
 #pragma unroll 1
                     for (int x = lane; x < 3 * 128; x += 32) nt->first[x / 128][x % 128] = 0x7fffffff;
-                    if (lane == 0) nt->nf_seg = seg;
+                    // the flag behind the reset: stream 0 may be in its epilogue already where
+                    // only stream 1 needs this tile
+                    __threadfence_block();
+                    __syncwarp();
+                    if (lane == 0) *(volatile int32_t*)&nt->nf_seg = seg;
                     __syncwarp();
                 }
                 // 16-byte chunk ch of row r sits at position ch ^ (r % 8) of its 128-byte row
@@ -703,7 +707,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                           ((int64_t)blockIdx.x * 2 + slot) * part_floats(D);
             const int row = (pair ? w * 128 : 0) + r;
             if (warp_live && (pair || w == 0)) {
-                const bool notes = steps && nt->nf_seg == seg;
+                const bool notes = steps && *(volatile int32_t*)&nt->nf_seg == seg;
                 const float inv = 1.f / l;
                 const int64_t orow = ((int64_t)(wk.b * (int64_t)a.max_new + tok) * c.hq +
                                       wk.h * G + (r & (G - 1)));
@@ -740,6 +744,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     __syncwarp();                       // the next load is the whole warp's
                 }
                 if (notes && live) {                    // rare: infinities and NaN that were seen
+                    __threadfence_block();              // the notes after their flag
 #pragma unroll 1
                     for (int i = 0; i < D; ++i) {
                         const float x = note_term(nt->first[0][i], nt->first[1][i], nt->first[2][i], pos);
@@ -751,6 +756,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                             part[(int64_t)row * D + i] += x;
                         }
                     }
+                    __threadfence_block();              // and before this warp is counted
                 }
                 if (live && whole) {
                     if (a.lse) a.lse[orow] = (m2 + log2f(l)) * 0.69314718055994531f;

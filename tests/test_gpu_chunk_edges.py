@@ -83,3 +83,24 @@ def test_infinities_of_units_that_follow_one_another(dtype, d, max_new):
         expect = torch.where(live[..., None, None], want[:, None, None], 0.0).expand_as(got)
         assert torch.equal(got.nan_to_num(nan=7.0), expect.nan_to_num(nan=7.0))
     assert kv.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinities_that_only_later_queries_see(dtype):
+    """Chunks of two query tiles that follow one another in a thread block, each with infinities
+    in the tokens that only its second tile's last queries see: its earlier rows, and those of
+    the next chunk, have none of them."""
+    batch, G, d, n = 330, 4, 64, 64                       # 256 rows: two tiles of 32 tokens
+    lens = [n + 64 * (b % 4) + 32 * (b % 2) for b in range(batch)]
+    kv, q = build(43, lens, n, G, 1, d, 64, dtype)
+    dims = torch.arange(batch, device="cuda") * 7 % d
+    for b, L in enumerate(lens):
+        put(kv, kv.v_pool, b, L - 1 - b % 16, int(dims[b]), INF)
+    first = n - 1 - torch.arange(batch, device="cuda") % 16     # the first query that sees it
+    seen = torch.arange(n, device="cuda")[None] >= first[:, None]
+    want = torch.zeros((batch, n, G, d), device="cuda")
+    want[torch.arange(batch), :, :, dims] = torch.where(seen, INF, 0.0)[..., None].expand(-1, -1, G)
+    for _ in range(5):
+        out, _ = run(kv, q, [n] * batch)
+        assert torch.equal(torch.where(torch.isfinite(out), 0.0, out.float()), want)
+    assert kv.status() == 0
