@@ -198,6 +198,7 @@ release_kernel(BlockPoolView p, const int32_t* keep_lens, int32_t* lens, int32_t
         return;
     }
     int64_t pushed = nfree;                     // stack height reached by earlier rounds
+    int64_t offered = nfree;                    // what it would be with the refused ones too
     for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int32_t first = 0, gone = 0, keep = -1;
@@ -229,7 +230,8 @@ release_kernel(BlockPoolView p, const int32_t* keep_lens, int32_t* lens, int32_t
             keep = -1;
         }
         int64_t total;
-        const int64_t end = pushed + block_scan(gone, warp_tot, &total);
+        const int64_t end = offered + block_scan(gone, warp_tot, &total);
+        offered += total;
         // more blocks than the pool has: something was given back twice; this sequence
         // and the ones after it are left as they are
         if (gone && end > p.num_phys) {
