@@ -122,12 +122,16 @@ __device__ __forceinline__ int bulk_count(const int32_t* n_new, int32_t max_new,
     return n < 0 ? 0 : (n > max_new ? max_new : n);
 }
 
+// What kernels earlier on the stream write (the tokens, the counts, the merge's partials) is
+// read after the dependency wait: none of it is __restrict__, which would let the compiler
+// take it for read-only during the whole kernel and load it before the wait.
+//
 // The input views tk, tv are [batch*max_new rows][Hkv][d] bf16 with boxes of 64
 // dimensions x 1 head x 64 tokens.
 __global__ void __launch_bounds__(kBulkThreads, 1)
 bulk_state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                  const __nv_bfloat16* __restrict__ k_new, const int32_t* __restrict__ n_new,
-                  int32_t max_new, int hkv, int tsplit, float* __restrict__ part,
+                  const __nv_bfloat16* k_new, const int32_t* n_new,
+                  int32_t max_new, int hkv, int tsplit, float* part,
                   int32_t* status) {
     extern __shared__ unsigned char bulk_smem_raw[];
     __shared__ __align__(8) uint64_t full[kBulkStages], ready[kBulkStages], empty[kBulkStages];
@@ -374,7 +378,7 @@ bulk_state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 // row 8 rg + r, lane l columns 4l .. 4l + 3. Partials are added in split order.
 __global__ void __launch_bounds__(256)
 bulk_merge_kernel(CacheView c, const int32_t* n_new, int32_t max_new, int splits, int tsplit,
-                  const float* __restrict__ part) {
+                  const float* part) {
     pdl_trigger();
     pdl_wait();
     const int bh = blockIdx.y;

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_sparse_linear_b200 import SplaBlockPool, _lib
+from block_sparse_linear_b200 import SplaBlockPool, SplaConfig, SplaDecodeCache, _lib
 
 from .test_gpu_block_plan import dev, make
 
@@ -36,3 +36,38 @@ def test_release_past_the_pool_leaves_every_later_sequence(at):
     np.testing.assert_array_equal(t[at:], table[at:])
     assert (t[:at] == -1).all()
     np.testing.assert_array_equal(pool.free_list.cpu().numpy()[count[0]:count[0] + at], table[:at, 0])
+
+
+def test_bulk_append_takes_the_counts_of_the_plan_before_it():
+    """A plan and the bulk append that reads its counts, back to back: whatever the buffer held
+    before, the append sees what the plan granted, and the state and pages are those of an append
+    with counts that were there from the start."""
+    cfg = SplaConfig(num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=64, top_k=4)
+    batch, mbp, max_new = 3, 40, 600
+    rng = np.random.default_rng(8)
+    g = torch.Generator("cuda").manual_seed(8)
+    pool = SplaBlockPool.empty(batch, mbp, batch * mbp, 64)
+    caches = [SplaDecodeCache(cfg, batch, pool.block_table, batch * mbp) for _ in range(2)]
+    for c in caches:
+        c.k_pool.zero_()
+        c.v_pool.zero_()
+    lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    after, granted = torch.zeros_like(lens), torch.zeros_like(lens)
+    stream = torch.cuda.current_stream().cuda_stream
+    for step in range(12):
+        n = dev(rng.integers(1, 200, batch) if step else [max_new, 1, 300])
+        k, v = (torch.randn((batch, max_new, 2, 128), device="cuda", generator=g).bfloat16()
+                for _ in "kv")
+        granted.fill_((0, max_new, max_new + 1)[step % 3])
+        torch.cuda.synchronize()
+        _lib.spla_block_plan(pool.c, lens.data_ptr(), n.data_ptr(), max_new, granted.data_ptr(),
+                             after.data_ptr(), 0, 0, pool.free_count.data_ptr(),
+                             pool.dev_status.data_ptr(), stream)
+        caches[1].append(k, v, granted, bulk=True)
+        lens.copy_(after)
+        torch.cuda.synchronize()
+        caches[0].append(k, v, n, bulk=True)
+        for name in ("k_pool", "v_pool", "blk_stats", "S", "z", "m", "context_lens"):
+            assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), (step, name)
+        assert torch.equal(caches[1].context_lens, lens)
+    assert pool.status() == 0 and [c.status() for c in caches] == [0, 0]
