@@ -239,7 +239,8 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
     row skipped; inv_freq: [rot_dim / 2] float64. Outputs, positions and slots may have any shape
     of that many elements. Keys and values go to k_out, v_out
     [rows][Hkv][d] (made here when not given), or with slots ([rows] int64) into the pools of
-    kv (a SplaPagedKV or SplaDecodeCache). Returns q_out, or (q_out, k_out, v_out) without
+    kv, a SplaPagedKV. (A SplaDecodeCache is refused: its pages are written by append, which
+    keeps the statistics, state and lengths in step with them.) Returns q_out, or (q_out, k_out, v_out) without
     slots; tensors made here hold zeros in skipped rows."""
     hq, hkv, d, dt, dev = (cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.torch_dtype,
                            q.device)
@@ -259,6 +260,9 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
         _need(k_gamma, "k_gamma", torch.float32, (d,), dev)
     if (slots is None) != (kv is None) or (kv is not None and (k_out is not None or v_out is not None)):
         raise ValueError("kv and slots go together, and without k_out and v_out")
+    if kv is not None and not isinstance(kv, SplaPagedKV):
+        raise ValueError(f"kv: expected a SplaPagedKV, got {type(kv).__name__} (a SplaDecodeCache "
+                         "takes keys and values by append)")
     if _elsewhere(dev, stream):
         with _at(dev, stream):
             return qk_norm_rope(cfg, q, k, v, positions, inv_freq, q_gamma, k_gamma, eps, interleaved,

@@ -405,7 +405,9 @@ SPLA_API spla_status spla_block_release(const spla_block_pool* pool, const int32
  *                 otherwise the pools [num_phys_blocks][Hkv][block_size][d], written at
  *                 slots[r] (spla_block_plan). A negative slot writes no key or value; one
  *                 past the pool sets SPLA_DEV_BAD_BLOCK_TABLE and writes none. Slots are
- *                 distinct. v_out may be NULL when v is.
+ *                 distinct. v_out may be NULL when v is. Only the pages are written: the
+ *                 pools of a cache that decodes sparsely are spla_append_kv's to write, which
+ *                 keeps its statistics, state and lengths in step with them.
  * Angles are taken in 64 bits, norms and rotations in 32, each output rounded once.
  * q, k, v, the outputs and gammas (read element by element) may not overlap the outputs;
  * q, k, v, q_out, k_out, v_out 16-byte aligned and strides a multiple of 16 bytes
