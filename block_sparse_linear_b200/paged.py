@@ -31,6 +31,8 @@ def _elsewhere(device, stream):
 
 
 def _at(device, stream):
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: one of {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
 
 

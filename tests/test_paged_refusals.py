@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from block_sparse_linear_b200 import SplaDecodeCache, qk_norm_rope
+from block_sparse_linear_b200 import SplaDecodeCache, paged, qk_norm_rope
 
 from .test_paged_host import _cfg, _kv
 
@@ -20,3 +20,10 @@ def test_norm_rope_writes_no_pages_of_a_sparse_cache():
     pos, slots = torch.zeros(6, dtype=torch.int32), torch.arange(6)
     with pytest.raises(ValueError, match="SplaPagedKV"):
         qk_norm_rope(cfg, rows, one, one, pos, kv=cache, slots=slots)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It cannot run work on these tensors; the call does not go to some other stream instead."""
+    here, other = torch.device("cuda", 0), torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream"):
+        paged._at(here, SimpleNamespace(device=other))
