@@ -1,4 +1,5 @@
 """What the paged serving calls refuse beside bad types and shapes, on the host."""
+from types import SimpleNamespace
 
 import pytest
 import torch
