@@ -287,7 +287,7 @@ cudaError_t launch_block_plan(const spla_block_pool* pool, const int32_t* lens,
                                max_new, n_granted, lens_after, positions, slots, free_out,
                                rows_inline, status);
     if (e != cudaSuccess || rows == 0 || rows_inline) return e;
-    const int tiles = (max_new + kRowsPerCta - 1) / kRowsPerCta;
+    const int tiles = (int)(((int64_t)max_new + kRowsPerCta - 1) / kRowsPerCta);
     return launch_pdl(plan_rows_kernel, dim3(tiles, p.batch < 65535 ? p.batch : 65535),
                       dim3(kRowsThreads), 0, s, p, lens, n_granted, max_new, positions, slots,
                       status);

@@ -71,3 +71,18 @@ def test_bulk_append_takes_the_counts_of_the_plan_before_it():
             assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), (step, name)
         assert torch.equal(caches[1].context_lens, lens)
     assert pool.status() == 0 and [c.status() for c in caches] == [0, 0]
+
+
+def test_plan_of_the_widest_rows():
+    """max_new up to 2^31 - 1 (batch 1): the row tiles are counted past 32 bits."""
+    max_new = 2 ** 31 - 1
+    pool = SplaBlockPool.empty(1, 8, 8, 64)
+    lens, n = dev([5]), dev([300])
+    granted, after = torch.zeros_like(n), torch.zeros_like(n)
+    pos = torch.full((max_new,), 7, dtype=torch.int32, device="cuda")
+    _lib.spla_block_plan(pool.c, lens.data_ptr(), n.data_ptr(), max_new, granted.data_ptr(),
+                         after.data_ptr(), pos.data_ptr(), 0, pool.free_count.data_ptr(),
+                         pool.dev_status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert granted.tolist() == [300] and after.tolist() == [305] and pool.status() == 0
+    assert torch.equal(pos[:300], torch.arange(5, 305, dtype=torch.int32, device="cuda"))
+    assert int(pos[300:].max()) == int(pos[300:].min()) == -1
