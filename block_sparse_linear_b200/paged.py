@@ -166,10 +166,13 @@ def chunk_attention(owner, q, n_new, out=None, lse=None, lens=None, stream=None)
     if owner._chunk_ws is None:
         need = _lib.spla_chunk_attention_workspace_size(p, b, T)
         owner._chunk_ws = torch.empty((need + 255) // 256 * 256, dtype=torch.uint8, device=dev)
-    ws = owner._chunk_ws
+        owner._chunk_ws_stream = _stream(dev)
+    ws, at = owner._chunk_ws, _stream(dev)
+    if at != owner._chunk_ws_stream:            # its memory is reused when this stream is done too
+        ws.record_stream(torch.cuda.current_stream(dev))
     _lib.spla_chunk_attention(p, c, q.data_ptr(), n_new.data_ptr(), T, out.data_ptr(),
                               _ptr(lse), ws.data_ptr(), ws.numel(), owner.dev_status.data_ptr(),
-                              _stream(dev))
+                              at)
     return out
 
 

@@ -6,6 +6,7 @@ import torch
 from block_sparse_linear_b200 import SplaBlockPool, SplaConfig, SplaDecodeCache, _lib
 
 from .test_gpu_block_plan import dev, make
+from .test_gpu_chunk_attention import build
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,24 @@ def test_plan_of_the_widest_rows():
     assert granted.tolist() == [300] and after.tolist() == [305] and pool.status() == 0
     assert torch.equal(pos[:300], torch.arange(5, 305, dtype=torch.int32, device="cuda"))
     assert int(pos[300:].max()) == int(pos[300:].min()) == -1
+
+
+def test_workspace_outlives_its_object_on_every_stream_it_was_used_on():
+    """The workspace a first call made on one stream, used on another: when the object goes while
+    that stream is still busy, nobody else gets the memory."""
+    kv, q = build(50, [3000], 4, 8, 2, 128, 64, "bf16")
+    n = dev([4])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = kv.chunk_attention(q, n, stream=side)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                     # 0.1 s of clocks on the current stream
+    got = kv.chunk_attention(q, n)
+    ws, size = kv._chunk_ws.data_ptr(), kv._chunk_ws.numel()
+    del kv
+    with torch.cuda.stream(side):
+        others = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert not torch.cuda.current_stream().query()     # the call is still to come
+    assert all(ws not in range(t.data_ptr(), t.data_ptr() + size) for t in others)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
