@@ -104,3 +104,85 @@ def test_infinities_that_only_later_queries_see(dtype):
         out, _ = run(kv, q, [n] * batch)
         assert torch.equal(torch.where(torch.isfinite(out), 0.0, out.float()), want)
     assert kv.status() == 0
+
+
+# ---- every token once: queries of zeros weigh all tokens alike, values count them by place
+def marked(kv):
+    """Values that name the 64 tokens they belong to: of KV head 0 the place modulo d, of head
+    1 the next digit. Slots past the lengths stay NaN."""
+    d, half = kv.cfg.head_dim, kv.cfg.block_size // 64
+    eye = torch.eye(d, dtype=kv.v_pool.dtype, device="cuda")
+    for b in range(kv.c.batch):
+        L = int(kv.context_lens[b])
+        pages = kv.block_table[b, :-(-L // kv.cfg.block_size)].long()
+        i = torch.arange(len(pages) * half, device="cuda")
+        for h, digit in enumerate((i % d, i // d % d)):
+            rows = eye[digit][:, None].expand(-1, 64, -1).reshape(len(pages), kv.cfg.block_size, d)
+            old = kv.v_pool[pages, h]
+            kv.v_pool[pages, h] = torch.where(torch.isnan(old), old, rows)
+
+
+def expected_counts(T, d):
+    """How many of the first T tokens bear each mark: float64 [...][2][d]."""
+    I, r = (T // 64)[..., None], (T % 64)[..., None].double()
+    j = torch.arange(d, device=T.device)
+    low = I // d + (j < I % d)
+    high = I // (d * d) * d + (I % (d * d) - j * d).clamp(0, d)
+    part = torch.stack((j == I % d, j == I // d % d), -2) * r[..., None]
+    return torch.stack((low, high), -2) * 64 + part
+
+
+def check_marks(kv, n_new, lens, max_new, rounds=1):
+    """q = 0: every probability is 1 and every sum a whole number below 2^24, so l and O are
+    exact in fp32. The result is O (1 / l): two roundings of 2^-24, and the store's; lse is
+    log2 l to a unit of its last place (2^-23) times ln 2, two more roundings."""
+    d, G = kv.cfg.head_dim, kv.cfg.num_q_heads // 2
+    q = torch.zeros((len(lens), max_new, 2 * G, d), dtype=kv.v_pool.dtype, device="cuda")
+    marked(kv)
+    n, L = (torch.tensor(x, device="cuda")[:, None] for x in (n_new, lens))
+    t = torch.arange(max_new, device="cuda")[None]
+    live = t < n
+    seen = torch.where(live, L - n + t + 1, 1)
+    counts = expected_counts(seen, d)
+    assert torch.equal(counts.sum(-1), seen[..., None].expand(-1, -1, 2).double())
+    want = (counts / seen[..., None, None])[:, :, :, None].expand(-1, -1, -1, G, -1).flatten(2, 3)
+    tol = want * (torch.finfo(q.dtype).eps / 2 * (q.dtype != torch.float32) + 2.0 ** -22)
+    want = torch.where(live[..., None, None], want, 5.0)
+    wz = torch.where(live, seen.double().log(), 5.0)[..., None]
+    for _ in range(rounds):
+        out, lse = run(kv, q, n_new)
+        bad = ((out.double() - want).abs() > torch.where(live[..., None, None], tol, 0.0)).nonzero()
+        assert len(bad) == 0, bad[:4]
+        bad = (lse.double() - wz).abs() > torch.where(live[..., None], 2.0 ** -22 * wz, 0.0)
+        assert not bad.any(), bad.nonzero()[:4]
+    assert kv.status() == 0
+
+
+@pytest.mark.parametrize("dtype,d,block,lens,n_new", [
+    ("bf16", 64, 64, [200003], [1]), ("bf16", 128, 128, [200003], [40]),
+    ("f32", 64, 64, [60001], [1]), ("f32", 128, 64, [60001], [40]),
+    ("bf16", 64, 64, [200003, 90, 130001], [1, 1, 1]), ("bf16", 128, 64, [200003, 90, 130001], [17, 3, 9]),
+    ("f32", 64, 64, [100001, 90, 65003], [1, 1, 0]), ("f32", 64, 128, [100001, 90, 65003], [17, 17, 17]),
+    ("bf16", 64, 128, [1048501], [1]), ("bf16", 64, 64, [70001], [1500]),
+    ("bf16", 128, 64, [262144, 4096, 131072, 8191, 65537, 16385, 32767, 100000],
+     [1, 33, 5, 2, 17, 1, 8, 64]),
+    ("f32", 64, 64, [5000, 40000, 777, 20011], [500, 200, 777, 1]),
+])
+def test_every_token_counts_once(dtype, d, block, lens, n_new):
+    """Long contexts over the whole GPU: a step that the split loses or takes twice changes lse
+    and the counts by far more than their roundings."""
+    kv, _ = build(44, lens, 1, 4, 2, d, block, dtype)
+    check_marks(kv, n_new, lens, max(n_new))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch", [400, 1000, 2500])
+@pytest.mark.parametrize("max_new", [1, 4, 70])
+def test_every_token_of_hundreds_of_sequences(dtype, batch, max_new):
+    """More sequences than a thread block has threads to scan them, some without new tokens, the
+    chunks of one query tile and of two."""
+    lens = [1 + (97 * i * i + 13 * i) % (90 if i % 17 else 1500) for i in range(batch)]
+    n_new = [0 if i % 6 == 5 else min(L, 1 + (i * 31) % max_new) for i, L in enumerate(lens)]
+    n_new[-1] = min(lens[-1], max_new)
+    kv, _ = build(45, lens, 1, 4, 2, 64, 64, dtype)
+    check_marks(kv, n_new, lens, max_new)
