@@ -26,10 +26,6 @@
 
 namespace spla {
 
-constexpr int kFKT = 64;                            // tokens of a step
-struct FCost {                                      // a unit's start and end take a step's time
-    static constexpr int kPair = 1, kOne = 1, kUnit = 1;
-};
 template <int WM> using FWalk = Walk<kFKT, FCost, (WM < 8)>;   // (WM < 8: one unit holds the chunk)
 
 template <int D, int WM>
@@ -359,7 +355,7 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
                 }
             }
         }
-        wk.note_cut(cut, U, G, run);
+        wk.note_cut(cut, blockIdx.x, U, G, run);
     }
     if (tid == 0) reinterpret_cast<ChunkCut*>(a.ws)[blockIdx.x] = cut;
 }

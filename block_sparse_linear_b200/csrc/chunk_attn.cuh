@@ -22,6 +22,9 @@
 
 #include "common.cuh"
 
+// The split's arithmetic also compiles for the host, where it is tested.
+#define SPLA_HD __host__ __device__ __forceinline__
+
 namespace spla {
 
 // What the split's run c left for the join, at its place in the workspace.
@@ -38,9 +41,9 @@ constexpr size_t kCutBytes = (sizeof(ChunkCut) * kMaxRuns + 255) / 256 * 256;
 // begins inside of, 1: of the unit it leaves unfinished).
 __host__ __device__ constexpr int64_t part_floats(int d) { return 256 * (int64_t)(d + 2); }
 
-// The chunk of sequence b; n = 0 where there is none or it is out of range.
-__device__ __forceinline__ void chunk_of(const CacheView& c, const ChunkArgs& a, int b,
-                                         int32_t* L, int32_t* n, bool flag) {
+// The chunk of sequence b; n = 0 where there is none or it is out of range, whose status
+// bit is returned.
+SPLA_HD int32_t chunk_of(const CacheView& c, const ChunkArgs& a, int b, int32_t* L, int32_t* n) {
     *L = c.lens[b];
     *n = a.n_new[b];
     int32_t bad = 0;
@@ -48,22 +51,24 @@ __device__ __forceinline__ void chunk_of(const CacheView& c, const ChunkArgs& a,
     else if (*L < 0 || *L > (int64_t)c.mbp * c.bs) bad = SPLA_DEV_CAPACITY;
     else if (*n > *L) bad = SPLA_DEV_BAD_COUNT;
     if (bad) {
-        if (flag) set_status(a.status, bad);
         *n = 0;
         *L = 0;
     }
+    return bad;
 }
 
 // Steps of the units before query block qb of a sequence whose chunk starts at position
 // base: sum over i < qb of ceil((base + (i+1) U) / KT). U and KT are powers of two.
 template <int KT>
-__device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U) {
+SPLA_HD int64_t steps_before(int32_t base, int32_t qb, int U) {
     if (U >= KT) {
         const int64_t k = U / KT;
         return (int64_t)qb * ((base + KT - 1) / KT) + k * ((int64_t)qb * (qb + 1) / 2);
     }
     // every r-th block of a class adds a step
-    const int lg = 31 - __clz(KT / U), r = 1 << lg;
+    int lg = 1;
+    while (U << lg < KT) ++lg;
+    const int r = 1 << lg;
     int64_t sum = 0;
 #pragma unroll 1
     for (int p = 0; p < r; ++p) {
@@ -72,6 +77,27 @@ __device__ __forceinline__ int64_t steps_before(int32_t base, int32_t qb, int U)
     }
     return sum;
 }
+
+// Tokens of a step and what steps cost: bf16.
+constexpr int kTcTile = 128;
+// A step of a pair of tiles against one of a single tile, and a unit's start and end, as
+// measured: with heads of 128 a pair's step takes its products' time (2.4 us), a single
+// tile's its bytes' (1.5 us), and 7:4 beats 3:2 (12 chunks of 1 to 200 tokens over 500 to
+// 30000: 210 us against 223; no difference where all units are alike); with heads of 64
+// 3:2 beats 7:4 (12 chunks of 1 to 1000 over 100 to 8000: 114 us against 124). A unit's
+// start and end take three to four steps of a single tile (24 prompts of 61 to 1500 tokens:
+// 101 us with 7 for 3:2, 107 with 4, 99 with 10).
+template <int D>
+struct TcCost {
+    static constexpr int kPair = D == 128 ? 7 : 3, kOne = D == 128 ? 4 : 2;
+    static constexpr int kUnit = D == 128 ? 14 : 7;
+};
+
+// The same, fp32: units of one tile, whose start and end take a step's time.
+constexpr int kFKT = 64;
+struct FCost {
+    static constexpr int kPair = 1, kOne = 1, kUnit = 1;
+};
 
 // A place in the row of all units' steps, and the walk over it that every role makes. A
 // unit's step 0 stands at its place F in the row, step j at F + start + j w, and a run has
@@ -90,28 +116,27 @@ struct Walk {
     int j0, j1, T, w;         // the current segment [j0, j1) of the unit's T steps of cost w
     int begin;                // what starting a unit costs
 
-    __device__ __forceinline__ static int units(int32_t n, int U) {
+    SPLA_HD static int units(int32_t n, int U) {
         return kSolo ? 1 : (n + U - 1) / U;
     }
     // Whether the unit's queries reach past its first tile.
-    __device__ __forceinline__ bool pair(int per_tile, int U) const {
+    SPLA_HD bool pair(int per_tile, int U) const {
         return !kSolo && (int64_t)qb * U + per_tile < n;
     }
-    __device__ __forceinline__ int start() const { return kSolo ? begin : Cost::kUnit; }
+    SPLA_HD int start() const { return kSolo ? begin : Cost::kUnit; }
     // Cost of a sequence's units before block qb, and of all of them, for one KV head (in
     // kSolo without the start).
-    __device__ __forceinline__ static int64_t cost_before(int32_t base, int32_t qb, int U) {
+    SPLA_HD static int64_t cost_before(int32_t base, int32_t qb, int U) {
         if (kSolo) return 0;
         return (int64_t)Cost::kUnit * qb + Cost::kPair * steps_before<KT>(base, qb, U);
     }
-    __device__ __forceinline__ static int64_t cost_of(int32_t L, int32_t n, int per_tile, int U) {
+    SPLA_HD static int64_t cost_of(int32_t L, int32_t n, int per_tile, int U) {
         const int q = units(n, U) - 1;
         const int w = !kSolo && (int64_t)q * U + per_tile < n ? Cost::kPair : Cost::kOne;
         return cost_before(L - n, q, U) + (kSolo ? 0 : Cost::kUnit) + (int64_t)w * ((L + KT - 1) / KT);
     }
     // Next segment of this run; false at its end.
-    __device__ __forceinline__ bool next(const CacheView& c, const ChunkArgs& a, int per_tile,
-                                         int U) {
+    SPLA_HD bool next(const CacheView& c, const ChunkArgs& a, int per_tile, int U) {
         if (j < 0) {                                  // the last unit is done: go to the next
             F += start() + (int64_t)T * w;
             j = 0;
@@ -126,7 +151,7 @@ struct Walk {
                             end = F;
                             return false;
                         }
-                        chunk_of(c, a, b, &L, &n, false);
+                        chunk_of(c, a, b, &L, &n);
                     }
                 }
             }
@@ -145,23 +170,87 @@ struct Walk {
         return true;
     }
     // Steps that query tile w of the unit takes part in end here.
-    __device__ __forceinline__ int tile_end(int w, int per_tile, int U) const {
+    SPLA_HD int tile_end(int w, int per_tile, int U) const {
         const int64_t t0 = (int64_t)qb * U + (int64_t)w * per_tile;
         if (t0 >= n) return 0;
         const int64_t last = L - n + min(t0 + per_tile, (int64_t)n);
         return min(j1, (int)((last + KT - 1) / KT));
     }
-    // For the join: what the current segment leaves when its unit starts in it and goes on
-    // past this run of length C.
-    __device__ __forceinline__ void note_cut(ChunkCut& cut, int U, int G, int64_t C) const {
+    // For the join: what the current segment of run `run` leaves when its unit starts in it and
+    // goes on past the run, of length C.
+    SPLA_HD void note_cut(ChunkCut& cut, int run, int U, int G, int64_t C) const {
         if (j0 != 0 || j1 >= T) return;
         // from the next run's start to the unit's last step: less than the unit's cost
-        const int64_t past = F + start() + (int64_t)(T - 1) * w - (int64_t)(blockIdx.x + 1) * C;
+        const int64_t past = F + start() + (int64_t)(T - 1) * w - (int64_t)(run + 1) * C;
         cut.parts = 2 + (past < C ? 0 : (int)((uint32_t)past / (uint32_t)C));
         cut.rows = (int)min((int64_t)U, n - (int64_t)qb * U) * G;
         cut.b = b;
         cut.h = h;
         cut.t0 = qb * U;
+    }
+
+    // ---- finding a run's start. kSolo: the units, 2^22 at most, are counted in the same sum,
+    // above the costs, which stay below 2^40: a bf16 sequence has 2^15 steps of kOne = 4 at
+    // most, an fp32 one 2^16 of 1.
+    static constexpr int64_t kSeq = kSolo ? 1ll << 40 : 0, kCosts = (1ll << 40) - 1;
+    SPLA_HD static int64_t weigh(int32_t L, int32_t n, int hkv, int per_tile, int U) {
+        return n ? hkv * (cost_of(L, n, per_tile, U) + kSeq) : 0;
+    }
+    // What starting a unit costs, by the sum over all sequences.
+    SPLA_HD static int begin_of(int64_t W) {
+        return kSolo && (W >> 40) < kMaxRuns && (W & kCosts) < 16 * Cost::kOne * kMaxRuns ? 0
+                                                                                          : Cost::kUnit;
+    }
+    // A sum of weigh() as a cost, the starts included.
+    SPLA_HD static int64_t total(int64_t sum, int begin) {
+        return kSolo ? (sum & kCosts) + begin * (sum >> 40) : sum;
+    }
+    SPLA_HD static int64_t run_length(int64_t W, int begin) {
+        // a run has the place of a step at least: steps stand no further apart
+        int64_t C = max((W + kMaxRuns - 1) / kMaxRuns,
+                        (int64_t)(begin + (kSolo ? Cost::kOne : max(Cost::kPair, Cost::kOne))));
+        // whole steps: as many in the longest run, and the others' ends, with them, in fewer
+        // units (one token over 4000: 17.5 us with runs of 7/4 steps, 15.8 with 8/4)
+        if (kSolo) C = (C + Cost::kOne - 1) / Cost::kOne * Cost::kOne;
+        return C;
+    }
+    // Goes to the run [f0, f0 + C) of all W, which starts `at` past the first unit of
+    // sequence b0, within the units of the `per` sequences from there.
+    SPLA_HD void seek(const CacheView& c, const ChunkArgs& a, int b0, int per, int64_t at,
+                      int64_t f0, int64_t C, int64_t W, int start_cost, int per_tile, int U) {
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) {
+            b = b0 + i;
+            chunk_of(c, a, b, &L, &n);
+            if (!n) continue;
+            const int32_t base = L - n;
+            const int64_t one = cost_of(L, n, per_tile, U) + (kSolo ? start_cost : 0);
+            if (at >= one * c.hkv) {
+                at -= one * c.hkv;
+                continue;
+            }
+#pragma unroll 1
+            for (h = 0; at >= one; ++h) at -= one;
+            int32_t lo = 0, hi = units(n, U) - 1;           // (kSolo: the block is 0)
+#pragma unroll 1
+            while (lo < hi) {
+                const int32_t mid = (lo + hi + 1) / 2;
+                if (cost_before(base, mid, U) <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            qb = lo;
+            at -= cost_before(base, lo, U);                 // how far into the unit the run starts
+            T = (int)((base + min((int64_t)(lo + 1) * U, (int64_t)n) + KT - 1) / KT);
+            w = pair(per_tile, U) ? Cost::kPair : Cost::kOne;
+            // the first step at or past that place, or the next unit
+            const int64_t past = at - start_cost;
+            j = at == 0 ? 0 : past <= w ? 1 : (int)(((uint32_t)past + w - 1) / w);
+            if (j >= T) j = -1;
+            break;
+        }
+        begin = start_cost;
+        F = f0 - at;
+        end = min(f0 + C, W);
     }
 };
 
@@ -175,17 +264,15 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
     using W_ = Walk<KT, Cost, kSolo>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
-    // kSolo: the units, 2^22 at most, are counted in the same scan, above the costs (all
-    // their steps, 2^16 at most each, stay below)
-    constexpr int64_t kSeq = kSolo ? 1ll << 40 : 0, kCosts = (1ll << 40) - 1;
     int64_t mine = 0;
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= c.batch) break;
         int32_t L, n;
-        chunk_of(c, a, b, &L, &n, blockIdx.x == 0);
-        if (n) mine += c.hkv * (W_::cost_of(L, n, per_tile, U) + kSeq);
+        const int32_t bad = chunk_of(c, a, b, &L, &n);
+        if (bad && blockIdx.x == 0) set_status(a.status, bad);
+        mine += W_::weigh(L, n, c.hkv, per_tile, U);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -201,56 +288,15 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         if (w < warp) upto += scan[w];
         W += scan[w];
     }
-    int begin = Cost::kUnit;
-    if (kSolo) {
-        if ((W >> 40) < kMaxRuns && (W & kCosts) < 16 * Cost::kOne * kMaxRuns) begin = 0;
-        W = (W & kCosts) + begin * (W >> 40);
-        mine = (mine & kCosts) + begin * (mine >> 40);
-        upto = (upto & kCosts) + begin * (upto >> 40);
-    }
-    // a run has the place of a step at least: steps stand no further apart
-    int64_t C = max((W + kMaxRuns - 1) / kMaxRuns,
-                    (int64_t)(begin + (kSolo ? Cost::kOne : max(Cost::kPair, Cost::kOne))));
-    // whole steps: as many in the longest run, and the others' ends, with them, in fewer
-    // units (one token over 4000: 17.5 us with runs of 7/4 steps, 15.8 with 8/4)
-    if (kSolo) C = (C + Cost::kOne - 1) / Cost::kOne * Cost::kOne;
+    const int begin = W_::begin_of(W);
+    W = W_::total(W, begin);
+    mine = W_::total(mine, begin);
+    upto = W_::total(upto, begin);
+    const int64_t C = W_::run_length(W, begin);
     const int64_t f0 = (int64_t)blockIdx.x * C;
     if (mine && f0 < W && upto - mine <= f0 && f0 < upto) {
-        int64_t at = f0 - (upto - mine);
         W_ w;
-#pragma unroll 1
-        for (int i = 0; i < per; ++i) {
-            w.b = tid * per + i;
-            chunk_of(c, a, w.b, &w.L, &w.n, false);
-            if (!w.n) continue;
-            const int32_t base = w.L - w.n;
-            const int64_t one = W_::cost_of(w.L, w.n, per_tile, U) + (kSolo ? begin : 0);
-            if (at >= one * c.hkv) {
-                at -= one * c.hkv;
-                continue;
-            }
-#pragma unroll 1
-            for (w.h = 0; at >= one; ++w.h) at -= one;
-            int32_t lo = 0, hi = W_::units(w.n, U) - 1;     // (kSolo: the block is 0)
-#pragma unroll 1
-            while (lo < hi) {
-                const int32_t mid = (lo + hi + 1) / 2;
-                if (W_::cost_before(base, mid, U) <= at) lo = mid;
-                else hi = mid - 1;
-            }
-            w.qb = lo;
-            at -= W_::cost_before(base, lo, U);       // how far into the unit the run starts
-            w.T = (int)((base + min((int64_t)(lo + 1) * U, (int64_t)w.n) + KT - 1) / KT);
-            w.w = w.pair(per_tile, U) ? Cost::kPair : Cost::kOne;
-            // the first step at or past that place, or the next unit
-            const int64_t past = at - begin;
-            w.j = at == 0 ? 0 : past <= w.w ? 1 : (int)(((uint32_t)past + w.w - 1) / w.w);
-            if (w.j >= w.T) w.j = -1;
-            break;
-        }
-        w.begin = begin;
-        w.F = f0 - at;
-        w.end = min(f0 + C, W);
+        w.seek(c, a, tid * per, per, f0 - (upto - mine), f0, C, W, begin, per_tile, U);
         *start = w;
         *run = C;
     }

@@ -35,7 +35,6 @@
 namespace spla {
 
 constexpr int kTcThreads = 384;
-constexpr int kTcTile = 128;                 // KV tokens of a step
 constexpr int kTcSmem = 227 * 1024;
 // Registers: the kernel is launched with 168 a thread; the softmax warps (a row of logits
 // each thread) take 216 and the other four give theirs down to 72. The shares add up to
@@ -200,18 +199,6 @@ __device__ __forceinline__ void tma_q(void* dst, const void* tmap, uint64_t* bar
         : "memory");
 }
 
-// A step of a pair of tiles against one of a single tile, and a unit's start and end, as
-// measured: with heads of 128 a pair's step takes its products' time (2.4 us), a single
-// tile's its bytes' (1.5 us), and 7:4 beats 3:2 (12 chunks of 1 to 200 tokens over 500 to
-// 30000: 210 us against 223; no difference where all units are alike); with heads of 64
-// 3:2 beats 7:4 (12 chunks of 1 to 1000 over 100 to 8000: 114 us against 124). A unit's
-// start and end take three to four steps of a single tile (24 prompts of 61 to 1500 tokens:
-// 101 us with 7 for 3:2, 107 with 4, 99 with 10).
-template <int D>
-struct TcCost {
-    static constexpr int kPair = D == 128 ? 7 : 3, kOne = D == 128 ? 4 : 2;
-    static constexpr int kUnit = D == 128 ? 14 : 7;
-};
 template <int D, bool kTwo> using TcWalk = Walk<kTcTile, TcCost<D>, !kTwo>;
 
 template <int D, bool kTwo>
@@ -765,7 +752,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     part[256 * D + 256 + row] = l;
                 }
             }
-            wk.note_cut(cut, U, G, nt->run);
+            wk.note_cut(cut, blockIdx.x, U, G, nt->run);
             tcf_before();
             __syncwarp();
             if (join && w == 0 && lane == 0) mbar_arrive(&nt->m_empty);
