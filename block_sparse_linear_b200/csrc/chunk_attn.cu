@@ -99,7 +99,7 @@ chunk_f32_kernel(const CacheView c, const ChunkArgs a) {
     }
     pdl_trigger();
     pdl_wait();
-    find_run<kFThreads>(c, a, U, U, scan, &start, &run);
+    find_run<kFThreads>(c, a, U, U, scan, first[0], &start, &run);
     FWalk<WM> wk = start;
     ChunkCut cut = {};
     auto ktile = [&](int s) { return f_smem + s * 2 * S::kTile; };

@@ -101,10 +101,16 @@ struct FCost {
 
 // A place in the row of all units' steps, and the walk over it that every role makes. A
 // unit's step 0 stands at its place F in the row, step j at F + start + j w, and a run has
-// the steps that stand in it. start is Cost::kUnit; with one unit per (sequence, KV head),
-// fewer of them than runs, and short runs, it is 0: every run starts a unit or goes on with
-// one, and those that start one would have no step besides. (Runs of hundreds of steps, 16
-// sequences of 4096 to 262144 tokens: 668 us with 0, 643 with Cost::kUnit.)
+// the steps that stand in it. start is Cost::kUnit; with one unit per (sequence, KV head)
+// and fewer of them than runs it is 0 where runs are shorter than three steps (those that start
+// a unit would have no step besides), or where the longest unit fits into a run (all are about
+// alike then, and each has a run for itself: nothing is cut). One token per sequence, bf16
+// heads of 128, us with 0 / with kUnit:
+//   runs of 2 steps: 8 units 14.8 / 15.9; 64 units of 0.2 to 1.8 times the mean 18.7 / 20.4;
+//   144 units alike, runs of 4, 8, 32 steps: 18.2 / 25.3, 22.0 / 28.4, 55.3 / 57.8;
+//   144 units of 0.2 to 1.8 times the mean, the same runs: 32.2 / 26.0, 38.1 / 29.4, 73.6 / 61.3;
+//   8 units, runs of 4, 8, 20 steps: 18.2 / 16.2, 23.1 / 21.0, 41.5 / 41.6.
+// Heads of 64 go the same way; fp32, whose start costs a step, differs by 5 % where not ragged.
 // per_tile: query tokens of an MMA tile, U or U / 2. kSolo: no chunk of the call has more
 // than one block of queries, of one tile (decode), which leaves little of the arithmetic.
 template <int KT, class Cost, bool kSolo>
@@ -196,10 +202,12 @@ struct Walk {
     SPLA_HD static int64_t weigh(int32_t L, int32_t n, int hkv, int per_tile, int U) {
         return n ? hkv * (cost_of(L, n, per_tile, U) + kSeq) : 0;
     }
-    // What starting a unit costs, by the sum over all sequences.
-    SPLA_HD static int begin_of(int64_t W) {
-        return kSolo && (W >> 40) < kMaxRuns && (W & kCosts) < 16 * Cost::kOne * kMaxRuns ? 0
-                                                                                          : Cost::kUnit;
+    // What starting a unit costs, by the sum over all sequences and the steps of the longest.
+    SPLA_HD static int begin_of(int64_t W, int longest) {
+        if (!kSolo || (W >> 40) >= kMaxRuns) return Cost::kUnit;
+        const int64_t steps = W & kCosts;
+        return steps < 3 * Cost::kOne * kMaxRuns ||
+                       (int64_t)longest * Cost::kOne <= run_length(steps, 0) ? 0 : Cost::kUnit;
     }
     // A sum of weigh() as a cost, the starts included.
     SPLA_HD static int64_t total(int64_t sum, int begin) {
@@ -256,15 +264,16 @@ struct Walk {
 
 // This CTA's place, by all NT threads of it: contiguous sequences per thread, a scan over
 // the CTA. *start (an empty run beforehand) and *run, its length, are for all after the
-// call; scan holds NT / 32 values. Two barriers.
+// call; scan and tops hold NT / 32 values each until then. Two barriers.
 template <int NT, int KT, class Cost, bool kSolo>
 __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a, int per_tile,
-                                         int U, int64_t* scan, Walk<KT, Cost, kSolo>* start,
-                                         int64_t* run) {
+                                         int U, int64_t* scan, int32_t* tops,
+                                         Walk<KT, Cost, kSolo>* start, int64_t* run) {
     using W_ = Walk<KT, Cost, kSolo>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((unsigned)c.batch + NT - 1) / NT;
     int64_t mine = 0;
+    int longest = 0;                                // (kSolo) steps of a unit
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
@@ -273,6 +282,7 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         const int32_t bad = chunk_of(c, a, b, &L, &n);
         if (bad && blockIdx.x == 0) set_status(a.status, bad);
         mine += W_::weigh(L, n, c.hkv, per_tile, U);
+        if (kSolo && n) longest = max(longest, (L + KT - 1) / KT);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -280,15 +290,20 @@ __device__ __forceinline__ void find_run(const CacheView& c, const ChunkArgs& a,
         const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
-    if (lane == 31) scan[warp] = upto;
+    if (kSolo) longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) {
+        scan[warp] = upto;
+        if (kSolo) tops[warp] = longest;
+    }
     __syncthreads();
     int64_t W = 0;
 #pragma unroll 4
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) upto += scan[w];
         W += scan[w];
+        if (kSolo) longest = max(longest, tops[w]);
     }
-    const int begin = W_::begin_of(W);
+    const int begin = W_::begin_of(W, longest);
     W = W_::total(W, begin);
     mine = W_::total(mine, begin);
     upto = W_::total(upto, begin);

@@ -292,7 +292,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     pdl_trigger();
 
     tcf_before();
-    find_run<kTcThreads>(c, a, per_tile, U, nt->scan, &nt->start, &nt->run);
+    find_run<kTcThreads>(c, a, per_tile, U, nt->scan, nt->first[0], &nt->start, &nt->run);
     tcf_after();
     const uint32_t tmem = nt->tmem;
     TcWalk<D, kTwo> wk = nt->start;

@@ -16,15 +16,17 @@ static int check(const CacheView& c, const ChunkArgs& a, int per_tile, int U, in
     const int per = (c.batch + NT - 1) / NT;
     std::vector<int64_t> mine(NT), upto(NT);
     int64_t sum = 0;
+    int longest_unit = 0;
     for (int t = 0; t < NT; ++t) {
         for (int i = 0; i < per && t * per + i < c.batch; ++i) {
             int32_t L, n;
             chunk_of(c, a, t * per + i, &L, &n);
             mine[t] += W_::weigh(L, n, c.hkv, per_tile, U);
+            if (n && (L + KT - 1) / KT > longest_unit) longest_unit = (L + KT - 1) / KT;
         }
         upto[t] = sum += mine[t];
     }
-    const int begin = W_::begin_of(sum);
+    const int begin = W_::begin_of(sum, longest_unit);
     const int64_t W = W_::total(sum, begin), C = W_::run_length(W, begin);
     for (int t = 0; t < NT; ++t) {
         mine[t] = W_::total(mine[t], begin);
