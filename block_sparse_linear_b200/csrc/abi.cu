@@ -734,7 +734,8 @@ spla_status spla_qk_norm_rope(const spla_params* params, const void* q, int64_t 
     if (misaligned16(q) || misaligned16(k) || misaligned16(v) || misaligned16(q_out) ||
         misaligned16(k_out) || misaligned16(v_out))
         return SPLA_ERR_INVALID_ARG;
-    // a row's heads are read and written by different threads
+    // No output over an input: which thread reads what before whom writes where is the kernel's
+    // own business. (A q_out in q's own layout would do no harm today; it is not promised.)
     const void* in[3] = {q, k, v};
     const uint64_t in_n[3] = {(uint64_t)((rows - 1) * q_stride + hq * d) * e,
                               (uint64_t)((rows - 1) * k_stride + hkv * d) * e,

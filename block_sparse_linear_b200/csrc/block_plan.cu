@@ -184,7 +184,9 @@ plan_rows_kernel(BlockPoolView p, const int32_t* lens, const int32_t* n_granted,
 }
 
 // Blocks past keep_lens[b] tokens go back to the stack; one CTA, a thread per sequence
-// for the scan, a warp per sequence for its entries.
+// for the scan, a warp per 32 sequences for their entries, one sequence after another (a look
+// over the entries, then the push). Bound by those rounds of loads in a row: a sequence of
+// 16384 blocks takes 109 us, 256 of 64 blocks 25 us, drafts given back about 10 us.
 __global__ void __launch_bounds__(kPlanThreads)
 release_kernel(BlockPoolView p, const int32_t* keep_lens, int32_t* lens, int32_t* status) {
     __shared__ int64_t warp_tot[kPlanWarps];

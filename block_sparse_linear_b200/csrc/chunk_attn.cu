@@ -7,8 +7,11 @@
 // a product, as fp32's own rounding is 2^-24 of a sum: the results are fp32 attention's
 // (tensor cores take tf32 at most, and fp32 FMAs have a quarter of this rate). mma.sync
 // m16n8k8 with the operands split in registers: the split parts of a tile would take twice
-// the shared memory, and these sizes are bound by the split's own instructions and by
-// shared-memory loads, not by the tensor pipe that tcgen05 would widen.
+// the shared memory. What that costs: every warp splits the whole K and V tile again, between
+// MMAs that wait for the parts. 512 tokens over 3584 (4/1 heads of 64) take 57 us with the tensor
+// pipe busy 47 % of the time and issue slots 37 %, warps waiting for one another's MMAs and for
+// the split; one token over each of 4 x 32768 (32/8 heads of 128) reads K and V at 2.9 TB/s, with
+// a two-stage ring and barriers of the whole CTA around each step.
 //
 // A CTA of 8 warps: WM of them side by side over rows (16 each), the others over the
 // tokens of a 64-token step, chosen so that few rows (decode) still use every warp; their

@@ -6,16 +6,17 @@
 // the head and the values pass through. Queries go out as rows; keys and values either
 // as rows (the append call's input) or straight into their pages by slot.
 //
-// Each element is read once and written once, so HBM bounds it, with the instructions per
-// element close behind: a group of d/16 lanes holds one head, 16 elements a lane, as two
+// Each element is read once and written once, so HBM bounds it, with the latency of a row's
+// loads behind it (16 warps of 128 registers an SM; their issue slots are busy 37 % of the
+// time, and warps mostly wait for loads): a group of d/16 lanes holds one head, 16 elements a lane, as two
 // 16-byte (bf16) loads whose positions are chosen so that every rotated pair lies within
 // one lane, and the group's lanes still cover whole 128-byte lines. A warp takes rows one
 // after another with two heads a lane in flight and no barrier wider than itself; scales,
 // cosines and sines are folded into four factors per pair once a row, and the arithmetic is
-// on pairs of fp32 (two to an instruction). With the arithmetic left out the same accesses
-// take 287 us for 65536 rows of 32 + 8 + 8 heads (5.6 TB/s); the kernel takes 340 us
-// (4.7 TB/s). Four heads in flight: 397 us (registers); 20 warps an SM instead of 16: 395 us
-// (spills); a CTA-wide table of sines, one thread per head share: 361 us.
+// on pairs of fp32 (two to an instruction). 65536 bf16 rows of 32 + 8 + 8 heads of 128, keys
+// and values into pages: 307 us (5.25 TB/s); with the arithmetic left out the same accesses
+// take 277 us. One head in flight 379 us, four 362 us (spills); 12 warps an SM 342 us, 20
+// 356 us (spills).
 // The angle is taken in 64 bits (a position near a million times a frequency near one
 // has lost five digits in 32) and reduced in turns, where the reduction is exact; a row's
 // sines and cosines are made once, by all lanes of its warp. Norms and rotations are fp32;

@@ -323,7 +323,9 @@ SPLA_API spla_status spla_block_causal_forward(const spla_params* params, const 
  * softmax attention (Baidu, section 1); the calls are the library's own.
  *
  * The pool of KV blocks. One block table and one pool may serve the caches of many
- * layers: every layer's k_pool and v_pool are indexed by the same physical blocks.
+ * layers: every layer's k_pool and v_pool are indexed by the same physical blocks. A block
+ * belongs to one sequence at a time. Calls on one pool are ordered on the GPU (one stream,
+ * or events), captured ones too.
  *   block_table : [batch][max_blocks_per_seq] int32, logical -> physical.
  *   free_list   : [num_phys_blocks] int32, a stack: entries 0 .. *free_count - 1 are the
  *                 blocks no sequence holds.
@@ -382,7 +384,9 @@ SPLA_API spla_status spla_block_plan(const spla_block_pool* pool, const int32_t*
  * SPLA_DEV_CAPACITY; each leaves that sequence (the last also the later ones that give
  * blocks back) unchanged. Only lengths and blocks change: statistics and the
  * linear-attention state of a spla_cache still hold what was appended, so a cache whose
- * layers decode sparsely releases whole sequences only.
+ * layers decode sparsely releases whole sequences only, and before a sequence is begun
+ * again its context_lens is 0 and its S, z and m are what spla_cache_init makes them
+ * (S = 0, z = 0, m = -infinity).
  */
 SPLA_API spla_status spla_block_release(const spla_block_pool* pool, const int32_t* keep_lens,
                                         int32_t* context_lens, int32_t* dev_status, void* stream);
@@ -435,9 +439,11 @@ SPLA_API spla_status spla_qk_norm_rope(const spla_params* params, const void* q,
  *   out    : [batch][max_new][Hq][d]; rows t >= n_new[b] are not written.
  *   lse    : [batch][max_new][Hq] fp32 or NULL: the natural log of each row's sum of
  *            exponentials (to merge with attention over other tokens).
- *   workspace : device scratch of at least spla_chunk_attention_workspace_size bytes,
- *            256-byte aligned, no initialisation; calls that share it are ordered on the
- *            GPU (one stream, or events), captured ones too.
+ *   workspace : device scratch of at least spla_chunk_attention_workspace_size bytes (39.4
+ *            MB for heads of 128, 20.0 MB for 64, whatever the batch and chunk), 256-byte
+ *            aligned, no initialisation; calls that share it are ordered on the GPU (one
+ *            stream, or events), captured ones too. Layers that run one after another may
+ *            share one.
  * Tokens past a sequence's length, and tokens after a query's own, have no part in its
  * result, whatever their slots hold. An infinity or NaN in a value that a query sees goes
  * into its result (an infinity may give NaN where its probability underflows); in a key or
