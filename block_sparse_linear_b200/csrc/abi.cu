@@ -684,7 +684,7 @@ spla_status spla_block_plan(const spla_block_pool* pool, const int32_t* context_
     spla_status st = check_pool(pool);
     if (st != SPLA_OK) return st;
     if (!context_lens || !n_new || !n_granted || !free_out || max_new < 0 ||
-        lens_after == context_lens || n_granted == context_lens)
+        lens_after == context_lens || n_granted == context_lens || n_granted == lens_after)
         return SPLA_ERR_INVALID_ARG;
     if ((int64_t)pool->batch * max_new > INT32_MAX) return SPLA_ERR_CAPACITY;
     cudaError_t e = launch_block_plan(pool, context_lens, n_new, max_new, n_granted, lens_after,

@@ -351,8 +351,8 @@ typedef struct {
  *   n_granted    : [batch] out: n_new[b], or 0 where the request is refused. It is the
  *                  n_new of the append or attention that follows; it may be the n_new
  *                  buffer itself.
- *   lens_after   : [batch] out or NULL: context_lens[b] + n_granted[b]; not the
- *                  context_lens buffer.
+ *   lens_after   : [batch] out or NULL: context_lens[b] + n_granted[b]; neither the
+ *                  context_lens nor the n_granted buffer.
  *   positions    : [batch][max_new] out or NULL: the new tokens' positions, -1 past
  *                  n_granted[b].
  *   slots        : [batch][max_new] int64 out or NULL: physical block * block_size +

@@ -1,4 +1,5 @@
 """What the paged serving calls refuse beside bad types and shapes, on the host."""
+import ctypes
 from types import SimpleNamespace
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 from block_sparse_linear_b200 import SplaDecodeCache, paged, qk_norm_rope
 
-from .test_paged_host import _cfg, _kv
+from .test_paged_host import INVALID, PLAN, _cfg, _kv, _pool
 
 
 def test_norm_rope_writes_no_pages_of_a_sparse_cache():
@@ -28,3 +29,9 @@ def test_a_stream_of_another_device_is_refused():
     here, other = torch.device("cuda", 0), torch.device("cuda", 1)
     with pytest.raises(ValueError, match="stream"):
         paged._at(here, SimpleNamespace(device=other))
+
+
+def test_plan_refuses_one_buffer_for_counts_and_lengths(lib):
+    """n_granted and lens_after in one buffer: the rows would follow the wrong one of them."""
+    a = {**PLAN, "lens_after": PLAN["n_granted"]}
+    assert lib.spla_block_plan(ctypes.byref(_pool()), *a.values(), None, None) == INVALID
