@@ -110,7 +110,8 @@ struct FCost {
 //   144 units alike, runs of 4, 8, 32 steps: 18.2 / 25.3, 22.0 / 28.4, 55.3 / 57.8;
 //   144 units of 0.2 to 1.8 times the mean, the same runs: 32.2 / 26.0, 38.1 / 29.4, 73.6 / 61.3;
 //   8 units, runs of 4, 8, 20 steps: 18.2 / 16.2, 23.1 / 21.0, 41.5 / 41.6.
-// Heads of 64 go the same way; fp32, whose start costs a step, differs by 5 % where not ragged.
+// Heads of 64 go the same way; in fp32, where a start costs a single step, units alike differ by
+// up to 7 % either way (12 % in runs of 2 steps), ragged ones lose up to 18 % with 0.
 // per_tile: query tokens of an MMA tile, U or U / 2. kSolo: no chunk of the call has more
 // than one block of queries, of one tile (decode), which leaves little of the arithmetic.
 template <int KT, class Cost, bool kSolo>

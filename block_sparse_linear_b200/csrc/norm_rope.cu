@@ -8,9 +8,9 @@
 //
 // Each element is read once and written once, so HBM bounds it, with the latency of a row's
 // loads behind it (16 warps of 128 registers an SM; their issue slots are busy 37 % of the
-// time, and warps mostly wait for loads): a group of d/16 lanes holds one head, 16 elements a lane, as two
-// 16-byte (bf16) loads whose positions are chosen so that every rotated pair lies within
-// one lane, and the group's lanes still cover whole 128-byte lines. A warp takes rows one
+// time, and warps mostly wait for loads): a group of d/16 lanes holds one head, 16 elements
+// a lane, as two 16-byte (bf16) loads whose positions are chosen so that every rotated pair
+// lies within one lane, and the group's lanes still cover whole 128-byte lines. A warp takes rows one
 // after another with two heads a lane in flight and no barrier wider than itself; scales,
 // cosines and sines are folded into four factors per pair once a row, and the arithmetic is
 // on pairs of fp32 (two to an instruction). 65536 bf16 rows of 32 + 8 + 8 heads of 128, keys

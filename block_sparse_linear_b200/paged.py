@@ -248,8 +248,8 @@ def qk_norm_rope(cfg, q, k, v, positions, inv_freq=None, q_gamma=None, k_gamma=N
     of that many elements. Keys and values go to k_out, v_out
     [rows][Hkv][d] (made here when not given), or with slots ([rows] int64) into the pools of
     kv, a SplaPagedKV. (A SplaDecodeCache is refused: its pages are written by append, which
-    keeps the statistics, state and lengths in step with them.) Returns q_out, or (q_out, k_out, v_out) without
-    slots; tensors made here hold zeros in skipped rows."""
+    keeps the statistics, state and lengths in step with them.) Returns q_out, or (q_out, k_out,
+    v_out) without slots; tensors made here hold zeros in skipped rows."""
     hq, hkv, d, dt, dev = (cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.torch_dtype,
                            q.device)
     rows = q.shape[0]
